@@ -3,8 +3,8 @@
 The compute lives in librlt.so (C ABI, include/rlt.h); this package is its thin
 Python binding plus the in-tree build script.
 """
-from .rlt import (RLTModel, RLTState, RLTError, lib, exported_names, make_config, LIB_PATH,
+from .rlt import (RLTModel, RLTState, RLTError, PagedBatch, lib, exported_names, make_config, LIB_PATH,
                   RLT_F32, RLT_BF16)
 
-__all__ = ["RLTModel", "RLTState", "RLTError", "lib", "exported_names", "make_config", "LIB_PATH",
+__all__ = ["RLTModel", "RLTState", "RLTError", "PagedBatch", "lib", "exported_names", "make_config", "LIB_PATH",
            "RLT_F32", "RLT_BF16"]

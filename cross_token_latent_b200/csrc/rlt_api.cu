@@ -1,6 +1,7 @@
 // C ABI of the RLT library (declared in include/rlt.h): model arena layout, weight
 // packing, the decoder-state registry and the encode / decode-step / replay drivers.
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -12,6 +13,7 @@
 
 #include "rlt.h"
 #include "kernels.cuh"
+#include "paged.cuh"
 
 using namespace rlt;
 
@@ -497,6 +499,124 @@ rlt_status encode_append_impl(rlt_model* m, const int32_t* tok, int tok_stride, 
             CK(launch_mem_layout<T>(L, qkv, B, 1, T_alloc, H, hd, M + g * group_elems + (size_t)pos * hd));
     }
     m->prof.end(p, st);
+    return RLT_OK;
+}
+
+// ------------------------------------------------------------------ paged cache
+// The kernels' description of a batch, after the checks that need no device.
+rlt_status paged_args(const rlt_model* m, const rlt_paged_batch* p, PagedArgs* out) {
+    if (!m || !p || p->B < 1 || p->N < 1 || p->max_q < 1 || p->max_q > p->N || p->max_kv < p->max_q) return RLT_EINVAL;
+    if (p->n_pages < 1 || p->n_kv_heads < 1 || p->table_stride < 1) return RLT_EINVAL;
+    if (p->max_kv > m->cfg.max_pos) return RLT_EINVAL;
+    int shift = 4;
+    while (shift <= 8 && (1 << shift) != p->page_size) ++shift;
+    if (shift > 8) return RLT_EINVAL;
+    if (((long long)p->max_kv + p->page_size - 1) / p->page_size > p->table_stride) return RLT_EINVAL;
+    PagedArgs a;
+    a.B = p->B; a.N = p->N; a.max_q = p->max_q; a.max_kv = p->max_kv;
+    a.q_start = p->q_start; a.kv_len = p->kv_len; a.table = p->table; a.table_stride = p->table_stride;
+    a.page_shift = shift; a.n_pages = p->n_pages; a.Hkv = p->n_kv_heads; a.hdr = m->hdr();
+    *out = a;
+    return RLT_OK;
+}
+// Checks of a call that launches: the device arrays, the current device, what the grids can count.
+rlt_status paged_launchable(const rlt_model* m, const rlt_paged_batch* p, int n_heads) {
+    if (!p->q_start || !p->kv_len || !p->table) return RLT_EINVAL;
+    if (!aligned(p->q_start, 4) || !aligned(p->kv_len, 4) || !aligned(p->table, 4)) return RLT_EINVAL;
+    int dev = -1;
+    CK(cudaGetDevice(&dev));
+    if (dev != m->device) return RLT_EINVAL;
+    const long long heads = n_heads > p->n_kv_heads ? n_heads : p->n_kv_heads;
+    if ((long long)p->N * heads + (long long)p->B * p->n_kv_heads > (1LL << 30)) return RLT_EUNSUPPORTED;
+    return RLT_OK;
+}
+bool rows_ok(const void* x, int64_t stride, int64_t row) {
+    return x && aligned(x, 16) && stride >= row && stride % 8 == 0;
+}
+rlt_status paged_attention(rlt_model* m, const PagedArgs& pa, const void* pool, const void* q, int64_t q_stride,
+                           int n_heads, void* out, int64_t out_stride, float scale, float* ws, cudaStream_t st) {
+    const rlt_config& c = m->cfg;
+    PagedAttnArgs a;
+    a.q = q; a.o = out; a.q_stride = q_stride; a.o_stride = out_stride; a.pool = pool;
+    a.H = n_heads; a.hd = c.head_dim;
+    a.scale = scale != 0.f ? scale : 1.0f / sqrtf((float)c.head_dim);
+    a.part = ws;
+    Launch L = m->launch(st);
+    if (c.dtype == RLT_BF16) CK(launch_paged_attention<bf16>(L, pa, a));
+    else CK(launch_paged_attention<float>(L, pa, a));
+    return RLT_OK;
+}
+
+struct ChunkWS {
+    size_t h, a, act, qkv, q, att, ews, part, total;
+};
+ChunkWS chunk_ws(const rlt_config& c, const PagedArgs& p) {
+    ChunkWS w;
+    const size_t N = p.N, d = c.d, e = c.dtype == RLT_BF16 ? 2 : 4;
+    size_t off = 0;
+    auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes); return o; };
+    w.h = take(N * d * 4);
+    w.a = take(N * d * e);
+    w.act = take(N * (size_t)c.F * e);
+    w.qkv = take(N * 3 * d * 4);
+    w.q = take(N * d * e);
+    w.att = take(N * d * e);
+    w.ews = take(N * d * e);
+    w.part = take(paged_attn_workspace(p, c.n_heads, c.head_dim, c.dtype == RLT_BF16));
+    w.total = off;
+    return w;
+}
+
+template <typename T>
+rlt_status encode_chunk_impl(rlt_model* m, const PagedArgs& p, const int32_t* tok, T* pools, T* e, T* M, int T_alloc,
+                             uint8_t* ws, cudaStream_t st) {
+    const rlt_config& c = m->cfg;
+    Launch L = m->launch(st);
+    const ChunkWS w = chunk_ws(c, p);
+    const int d = c.d, F = c.F, H = c.n_heads, hd = c.head_dim, N = p.N;
+    float* h = reinterpret_cast<float*>(ws + w.h);
+    T* a = reinterpret_cast<T*>(ws + w.a);
+    T* act = reinterpret_cast<T*>(ws + w.act);
+    float* qkv = reinterpret_cast<float*>(ws + w.qkv);
+    T* q = reinterpret_cast<T*>(ws + w.q);
+    T* att = reinterpret_cast<T*>(ws + w.att);
+    T* ews = reinterpret_cast<T*>(ws + w.ews);
+    float* part = reinterpret_cast<float*>(ws + w.part);
+    const size_t layer = ((size_t)p.n_pages * 2 * H << p.page_shift) * hd;
+    const int prof = m->prof.begin(RLT_K_ENCODER, st);
+    CK(launch_embed<T>(L, tok, N, m->at<T>(m->lay.embed), c.V, d, h, m->hdr()));
+    for (int l = 0; l < c.L_E; ++l) {
+        T* pool = pools + (size_t)l * layer;
+        EpiArgs ea; ea.hdr = m->hdr();
+        CK(launch_rmsnorm<T>(L, h, N, d, m->at<float>(m->lay.attn_norm[l]), c.rms_eps, a, d, N, N, nullptr));
+        ea.out_f32 = qkv; ea.ld_out = 3 * d;
+        CK(launch_gemm<T>(L, Epi::StoreF32, a, d, m->at<T>(m->lay.wqkv[l]), N, 3 * d, d, ea));
+        AppendArgs ap;
+        ap.q = qkv; ap.k = qkv + d; ap.v = qkv + 2 * d;
+        ap.q_stride = ap.k_stride = ap.v_stride = 3 * d;
+        ap.q_out = q; ap.q_out_stride = d;
+        ap.H = H; ap.pool = pool; ap.rope = m->at<float2>(m->lay.rope); ap.hd = hd;
+        CK((launch_paged_append<T, float>(L, p, ap)));
+        const rlt_status s = paged_attention(m, p, pool, q, d, H, att, d, 0.f, part, st);
+        if (s != RLT_OK) return s;
+        ea = EpiArgs(); ea.hdr = m->hdr(); ea.out_f32 = h; ea.ld_out = d;
+        CK(launch_gemm<T>(L, Epi::ResidAdd, att, d, m->at<T>(m->lay.wo[l]), N, d, d, ea));
+        CK(launch_rmsnorm<T>(L, h, N, d, m->at<float>(m->lay.ffn_norm[l]), c.rms_eps, a, d, N, N, nullptr));
+        ea = EpiArgs(); ea.hdr = m->hdr(); ea.out_t = act; ea.ld_out = F;
+        CK(launch_gemm<T>(L, Epi::SwiGLU, a, d, m->at<T>(m->lay.wgu[l]), N, 2 * F, d, ea));
+        ea = EpiArgs(); ea.hdr = m->hdr(); ea.out_f32 = h; ea.ld_out = d;
+        CK(launch_gemm<T>(L, Epi::ResidAdd, act, F, m->at<T>(m->lay.wdown[l]), N, d, F, ea));
+    }
+    CK(launch_rmsnorm<T>(L, h, N, d, m->at<float>(m->lay.enc_norm), c.rms_eps, ews, d, N, N, nullptr));
+    CK(launch_paged_scatter_e<T>(L, p, ews, d, e, T_alloc));
+    const size_t group_elems = (size_t)2 * p.B * H * (size_t)T_alloc * hd;
+    for (int g = 0; g < c.G; ++g) {
+        EpiArgs ea; ea.hdr = m->hdr();
+        ea.out_f32 = qkv; ea.ld_out = 2 * d;
+        CK(launch_gemm<T>(L, Epi::StoreF32, ews, d, m->at<T>(m->lay.mem) + (size_t)g * 2 * d * d, N, 2 * d, d, ea));
+        CK(launch_paged_scatter_m<T>(L, p, qkv, H, hd, M + g * group_elems, T_alloc));
+    }
+    m->prof.end(prof, st);
     return RLT_OK;
 }
 
@@ -1146,6 +1266,117 @@ rlt_status rlt_sample(rlt_model* m, const float* logp, int B, const float* u, in
     if (m->cfg.V > sample_max_vocab()) return RLT_EUNSUPPORTED;
     Launch L = m->launch(stream);
     CK(launch_sample(L, logp, B, m->cfg.V, u, top_k, top_p, tokens, tok_stride, behaviour_logp));
+    return RLT_OK;
+}
+
+// ---------------------------------------------------------------- paged cache, logits
+size_t rlt_page_pool_bytes(const rlt_model* m, int n_pages, int page_size, int n_kv_heads) {
+    if (!m || n_pages < 1 || page_size < 1 || n_kv_heads < 1) return 0;
+    return (size_t)n_pages * 2 * n_kv_heads * page_size * m->cfg.head_dim * m->lay.esz;
+}
+
+rlt_status rlt_paged_append(rlt_model* m, const rlt_paged_batch* p, void* pool, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const void* q, int64_t q_stride, int n_heads,
+                            void* q_out, int64_t q_out_stride, int src_dtype, void* stream) {
+    PagedArgs pa;
+    rlt_status s = paged_args(m, p, &pa);
+    if (s != RLT_OK) return s;
+    const rlt_config& c = m->cfg;
+    if (!pool || !aligned(pool) || !q != !q_out || (q && n_heads < 1)) return RLT_EINVAL;
+    if (src_dtype != RLT_F32 && !(src_dtype == RLT_BF16 && c.dtype == RLT_BF16)) return RLT_EINVAL;
+    const int64_t kv_row = (int64_t)p->n_kv_heads * c.head_dim, q_row = (int64_t)n_heads * c.head_dim;
+    if (!rows_ok(k, k_stride, kv_row) || !rows_ok(v, v_stride, kv_row)) return RLT_EINVAL;
+    if (q && (!rows_ok(q, q_stride, q_row) || !rows_ok(q_out, q_out_stride, q_row))) return RLT_EINVAL;
+    if (q == q_out && q && (src_dtype != c.dtype || q_stride != q_out_stride)) return RLT_EINVAL;
+    s = paged_launchable(m, p, q ? n_heads : 0);
+    if (s != RLT_OK) return s;
+    AppendArgs a;
+    a.k = k; a.v = v; a.q = q; a.q_out = q_out;
+    a.k_stride = k_stride; a.v_stride = v_stride; a.q_stride = q_stride; a.q_out_stride = q_out_stride;
+    a.H = q ? n_heads : 0; a.pool = pool; a.rope = m->at<float2>(m->lay.rope); a.hd = c.head_dim;
+    Launch L = m->launch(stream);
+    if (c.dtype == RLT_F32) CK((launch_paged_append<float, float>(L, pa, a)));
+    else if (src_dtype == RLT_F32) CK((launch_paged_append<bf16, float>(L, pa, a)));
+    else CK((launch_paged_append<bf16, bf16>(L, pa, a)));
+    return RLT_OK;
+}
+
+size_t rlt_paged_attention_workspace_bytes(const rlt_model* m, const rlt_paged_batch* p, int n_heads) {
+    PagedArgs pa;
+    if (paged_args(m, p, &pa) != RLT_OK || n_heads < 1 || n_heads % p->n_kv_heads) return 0;
+    return paged_attn_workspace(pa, n_heads, m->cfg.head_dim, m->cfg.dtype == RLT_BF16);
+}
+
+rlt_status rlt_paged_attention(rlt_model* m, const rlt_paged_batch* p, const void* pool, const void* q,
+                               int64_t q_stride, int n_heads, void* out, int64_t out_stride, float scale, void* ws,
+                               size_t ws_bytes, void* stream) {
+    PagedArgs pa;
+    rlt_status s = paged_args(m, p, &pa);
+    if (s != RLT_OK) return s;
+    const rlt_config& c = m->cfg;
+    if (!pool || !aligned(pool) || n_heads < 1 || !(scale >= 0.f) || std::isinf(scale)) return RLT_EINVAL;
+    if (n_heads % p->n_kv_heads || n_heads / p->n_kv_heads > 64) return RLT_EUNSUPPORTED;
+    const int64_t row = (int64_t)n_heads * c.head_dim;
+    if (!rows_ok(q, q_stride, row) || !rows_ok(out, out_stride, row)) return RLT_EINVAL;
+    s = paged_launchable(m, p, n_heads);
+    if (s != RLT_OK) return s;
+    const size_t need = paged_attn_workspace(pa, n_heads, c.head_dim, c.dtype == RLT_BF16);
+    if (need > 0 && (!ws || !aligned(ws) || ws_bytes < need)) return RLT_EINVAL;
+    return paged_attention(m, pa, pool, q, q_stride, n_heads, out, out_stride, scale, reinterpret_cast<float*>(ws),
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t rlt_encode_chunk_workspace_bytes(const rlt_model* m, const rlt_paged_batch* p) {
+    PagedArgs pa;
+    if (paged_args(m, p, &pa) != RLT_OK || p->n_kv_heads != m->cfg.n_heads) return 0;
+    return chunk_ws(m->cfg, pa).total;
+}
+
+rlt_status rlt_encode_chunk(rlt_model* m, const rlt_paged_batch* p, const int32_t* tokens, void* pools, void* e,
+                            void* M, int T_alloc, void* ws, size_t ws_bytes, void* stream) {
+    PagedArgs pa;
+    rlt_status s = paged_args(m, p, &pa);
+    if (s != RLT_OK) return s;
+    if (!tokens || !pools || !e || !M || !ws || m->version == 0) return RLT_EINVAL;
+    if (p->n_kv_heads != m->cfg.n_heads || p->max_kv > T_alloc || T_alloc > m->cfg.max_pos) return RLT_EINVAL;
+    if (!aligned(tokens, 4) || !aligned(pools) || !aligned(e) || !aligned(M) || !aligned(ws)) return RLT_EINVAL;
+    s = paged_launchable(m, p, m->cfg.n_heads);
+    if (s != RLT_OK) return s;
+    if (ws_bytes < chunk_ws(m->cfg, pa).total) return RLT_EINVAL;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+    return m->cfg.dtype == RLT_BF16
+        ? encode_chunk_impl<bf16>(m, pa, tokens, (bf16*)pools, (bf16*)e, (bf16*)M, T_alloc, w, st)
+        : encode_chunk_impl<float>(m, pa, tokens, (float*)pools, (float*)e, (float*)M, T_alloc, w, st);
+}
+
+rlt_status rlt_process_logits(rlt_model* m, const rlt_logits* a, int B, void* stream) {
+    if (!m || !a || !a->x || !a->out || B < 1) return RLT_EINVAL;
+    const int V = m->cfg.V;
+    const int64_t words = (V + 31) / 32;
+    if (a->x_stride < V || a->out_stride < V || (a->bias && a->bias_stride != 0 && a->bias_stride < V) ||
+        (a->mask && a->mask_stride != 0 && a->mask_stride < words))
+        return RLT_EINVAL;
+    if (a->out == a->x && a->out_stride != a->x_stride) return RLT_EINVAL;
+    if (a->tokens && (a->n_tokens < 0 || a->seq_stride < 0 || a->tok_stride < 0)) return RLT_EINVAL;
+    for (const void* x : {(const void*)a->x, (const void*)a->out, (const void*)a->lse, (const void*)a->bias,
+                          (const void*)a->mask, (const void*)a->tokens, (const void*)a->tok_len,
+                          (const void*)a->gen_start, (const void*)a->repetition, (const void*)a->presence,
+                          (const void*)a->frequency, (const void*)a->tau, (const void*)a->out_lse})
+        if (x && !aligned(x, 4)) return RLT_EINVAL;
+    if (V > logits_max_vocab() || B > (1 << 27)) return RLT_EUNSUPPORTED;
+    int dev = -1;
+    CK(cudaGetDevice(&dev));
+    if (dev != m->device) return RLT_EINVAL;
+    LogitsArgs g;
+    g.x = a->x; g.x_stride = a->x_stride; g.out = a->out; g.out_stride = a->out_stride; g.B = B; g.V = V;
+    g.lse = a->lse; g.bias = a->bias; g.bias_stride = a->bias_stride; g.mask = a->mask; g.mask_stride = a->mask_stride;
+    g.tokens = a->n_tokens > 0 ? a->tokens : nullptr;
+    g.seq_stride = a->seq_stride; g.tok_stride = a->tok_stride; g.n_tokens = a->n_tokens;
+    g.tok_len = a->tok_len; g.gen_start = a->gen_start; g.repetition = a->repetition; g.presence = a->presence;
+    g.frequency = a->frequency; g.tau = a->tau; g.out_lse = a->out_lse; g.hdr = m->hdr();
+    Launch L = m->launch(stream);
+    CK(launch_process_logits(L, g));
     return RLT_OK;
 }
 

@@ -33,6 +33,22 @@ class Config(ctypes.Structure):
                [("rms_eps", ctypes.c_float), ("rope_base", ctypes.c_float), ("max_pos", ctypes.c_int32)]
 
 
+class PagedBatchArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "N", "max_q", "max_kv")] + \
+               [(n, ctypes.c_void_p) for n in ("q_start", "kv_len", "table")] + \
+               [(n, ctypes.c_int32) for n in ("table_stride", "page_size", "n_pages", "n_kv_heads")]
+
+
+class LogitsArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("lse", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("bias_stride", ctypes.c_int64), ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("tok_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int32), ("tok_len", ctypes.c_void_p), ("gen_start", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("tau", ctypes.c_void_p), ("out_lse", ctypes.c_void_p)]
+
+
 _lib = None
 _EXPORTS = {
     "rlt_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -59,6 +75,20 @@ _EXPORTS = {
                                          ctypes.c_void_p]),
     "rlt_sample": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
                                   ctypes.c_float, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
+    "rlt_page_pool_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "rlt_paged_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+                                        ctypes.c_void_p]),
+    "rlt_paged_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int]),
+    "rlt_paged_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,
+                                           ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "rlt_encode_chunk_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_void_p]),
+    "rlt_encode_chunk": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                        ctypes.c_size_t, ctypes.c_void_p]),
+    "rlt_process_logits": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
     "rlt_state_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int]),
     "rlt_state_positions_offset": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int]),
     "rlt_state_positions": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_int64)]),
@@ -193,6 +223,51 @@ class RLTState:
             pass
 
 
+def _need(t: torch.Tensor, what: str, dtype, device, shape) -> None:
+    """ValueError unless t is a tensor of this type, device and shape (None: any size)."""
+    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what}: need {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _row_stride(t: torch.Tensor, what: str) -> int:
+    """Elements between the rows of [N, heads, head_dim], whose rows are contiguous."""
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what}: the heads of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+class PagedBatch:
+    """The new tokens of a ragged batch over a paged key/value cache (rlt_paged_batch in
+    include/rlt.h): its device arrays and the bounds the host knows.  Made once and used for every
+    layer; what the device arrays hold may change between calls."""
+
+    def __init__(self, model: "RLTModel", table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, N: int,
+                 max_q: int, max_kv: int, page_size: int, n_kv_heads: int):
+        B = kv_len.shape[0]
+        _need(table, "table", torch.int32, model.device, (B, None))
+        _need(q_start, "q_start", torch.int32, model.device, (B + 1,))
+        _need(kv_len, "kv_len", torch.int32, model.device, (B,))
+        if not (q_start.is_contiguous() and kv_len.is_contiguous()) or table.stride(1) != 1 or \
+                table.stride(0) < table.shape[1]:
+            raise ValueError("q_start, kv_len and the rows of the page table must be contiguous")
+        cols = table.shape[1]
+        if not (1 <= max_q <= N and max_q <= max_kv <= min(model.max_pos, cols * page_size)):
+            raise ValueError(f"need 1 <= max_q <= N and max_q <= max_kv <= min(max_pos, {cols} pages): "
+                             f"got N {N}, max_q {max_q}, max_kv {max_kv}")
+        self.model, self.B, self.N = model, B, int(N)
+        self.page_size, self.n_kv_heads = int(page_size), int(n_kv_heads)
+        self.table, self.q_start, self.kv_len = table, q_start, kv_len
+        self.c = PagedBatchArgs(B, int(N), int(max_q), int(max_kv), q_start.data_ptr(), kv_len.data_ptr(),
+                                table.data_ptr(), table.stride(0) if B > 1 else cols, int(page_size), 0,
+                                int(n_kv_heads))
+        self.ref = ctypes.byref(self.c)
+
+    def args(self, n_pages: int):
+        self.c.n_pages = n_pages
+        return self.ref
+
+
 class RLTModel:
     """One model on one CUDA device: weight arena, encoder, decoder step and replay."""
 
@@ -201,6 +276,8 @@ class RLTModel:
             raise RuntimeError("RLTModel needs a CUDA device")
         self.cfg = cfg
         self.device = torch.device(device)
+        if self.device.index is None:
+            self.device = torch.device(self.device.type, torch.cuda.current_device())
         self.max_pos = int(max_pos)
         self.sdtype = torch.bfloat16 if cfg.dtype == "bf16" else torch.float32
         self._c = make_config(cfg, max_pos)
@@ -336,14 +413,160 @@ class RLTModel:
                                 out.stride(0), _ptr(behaviour_logp), _stream()), "rlt_sample")
         return out
 
+    # ---------------------------------------------------------------- paged cache
+    def alloc_pages(self, n_pages: int, page_size: int, n_kv_heads: int | None = None,
+                    layers: int | None = None) -> torch.Tensor:
+        """Pools of pages, [layers, n_pages, 2, n_kv_heads, page_size, head_dim] (defaults: the model's)."""
+        c = self.cfg
+        return torch.empty((c.L_E if layers is None else layers, n_pages, 2, n_kv_heads or c.n_heads, page_size,
+                            c.head_dim), dtype=self.sdtype, device=self.device)
+
+    def paged_batch(self, table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, N: int, max_q: int,
+                    max_kv: int, page_size: int, n_kv_heads: int | None = None) -> PagedBatch:
+        """Describe new tokens over a paged cache: table int32 [B, pages], q_start int32 [B + 1], kv_len
+        int32 [B] (with the new tokens), N packed rows, and bounds of every sequence's new tokens and
+        kv_len."""
+        return PagedBatch(self, table, q_start, kv_len, N, max_q, max_kv, page_size,
+                          self.cfg.n_heads if n_kv_heads is None else n_kv_heads)
+
+    def _pool(self, batch: PagedBatch, pool: torch.Tensor):
+        if batch.model is not self:
+            raise ValueError("the batch was made for another model")
+        _need(pool, "pool", self.sdtype, self.device, (None, 2, batch.n_kv_heads, batch.page_size, self.cfg.head_dim))
+        if not pool.is_contiguous():
+            raise ValueError("pool: must be contiguous")
+        return batch.args(pool.shape[0])
+
+    def paged_append(self, batch: PagedBatch, pool: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     q: torch.Tensor | None = None, q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+        """rlt_paged_append: k, v [N, n_kv_heads, head_dim] (float32 or the model's dtype) into the pool
+        [n_pages, 2, n_kv_heads, page_size, head_dim], the keys rotated; with q [N, n_heads, head_dim] the
+        rotated queries are returned (in q_out)."""
+        ref = self._pool(batch, pool)
+        N, hd = batch.N, self.cfg.head_dim
+        if k.dtype != torch.float32 and k.dtype != self.sdtype:
+            raise ValueError(f"k: need float32 or {self.sdtype}, got {k.dtype}")
+        _need(k, "k", k.dtype, self.device, (N, batch.n_kv_heads, hd))
+        _need(v, "v", k.dtype, self.device, (N, batch.n_kv_heads, hd))
+        H = qs = os = 0
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+        else:
+            H = q.shape[1]
+            _need(q, "q", k.dtype, self.device, (N, None, hd))
+            if q_out is None:
+                q_out = torch.empty((N, H, hd), dtype=self.sdtype, device=self.device)
+            _need(q_out, "q_out", self.sdtype, self.device, (N, H, hd))
+            qs, os = _row_stride(q, "q"), _row_stride(q_out, "q_out")
+        _check(lib().rlt_paged_append(self.handle, ref, pool.data_ptr(), k.data_ptr(), _row_stride(k, "k"),
+                                      v.data_ptr(), _row_stride(v, "v"), _ptr(q), qs, H, _ptr(q_out), os,
+                                      RLT_F32 if k.dtype == torch.float32 else RLT_BF16, _stream()),
+               "rlt_paged_append")
+        return q_out
+
+    def paged_attention(self, batch: PagedBatch, pool: torch.Tensor, q: torch.Tensor, out: torch.Tensor | None = None,
+                        scale: float = 0.0) -> torch.Tensor:
+        """rlt_paged_attention: q [N, n_heads, head_dim] (rotated, the model's dtype) over the pool, which
+        holds the new tokens already -> out, the same shape (rows behind the last sequence are left as
+        they were).  scale 0: 1 / sqrt(head_dim)."""
+        ref = self._pool(batch, pool)
+        H = q.shape[1]
+        _need(q, "q", self.sdtype, self.device, (batch.N, None, self.cfg.head_dim))
+        if out is None:
+            out = torch.empty((batch.N, H, self.cfg.head_dim), dtype=self.sdtype, device=self.device)
+        _need(out, "out", self.sdtype, self.device, (batch.N, H, self.cfg.head_dim))
+        # the workspace is the caller's stream's: from torch's allocator, for this call alone
+        nb = lib().rlt_paged_attention_workspace_bytes(self.handle, ref, H)
+        ws = torch.empty(nb, dtype=torch.uint8, device=self.device) if nb else None
+        _check(lib().rlt_paged_attention(self.handle, ref, pool.data_ptr(), q.data_ptr(), _row_stride(q, "q"), H,
+                                         out.data_ptr(), _row_stride(out, "out"), float(scale), _ptr(ws), nb,
+                                         _stream()), "rlt_paged_attention")
+        return out
+
+    def encode_chunk(self, batch: PagedBatch, pools: torch.Tensor, tokens: torch.Tensor, e: torch.Tensor,
+                     M: torch.Tensor) -> None:
+        """rlt_encode_chunk: encode tokens int32 [N] over pools (alloc_pages); the new rows of e
+        [B, T_alloc, d] and M [G, 2, B, n_heads, T_alloc, head_dim] are written in place."""
+        c = self.cfg
+        _need(pools, "pools", self.sdtype, self.device, (c.L_E, None, 2, c.n_heads, batch.page_size, c.head_dim))
+        ref = self._pool(batch, pools[0])
+        _need(tokens, "tokens", torch.int32, self.device, (batch.N,))
+        _need(e, "e", self.sdtype, self.device, (batch.B, None, c.d))
+        _need(M, "M", self.sdtype, self.device, (c.G, 2, batch.B, c.n_heads, e.shape[1], c.head_dim))
+        if not (pools.is_contiguous() and tokens.is_contiguous() and e.is_contiguous() and M.is_contiguous()):
+            raise ValueError("pools, tokens, e and M must be contiguous")
+        nb = lib().rlt_encode_chunk_workspace_bytes(self.handle, ref)
+        ws = torch.empty(max(nb, 256), dtype=torch.uint8, device=self.device)
+        _check(lib().rlt_encode_chunk(self.handle, ref, _ptr(tokens), _ptr(pools), _ptr(e), _ptr(M), e.shape[1],
+                                      _ptr(ws), nb, _stream()), "rlt_encode_chunk")
+
+    # ---------------------------------------------------------------- logits before a draw
+    def process_logits(self, logits: torch.Tensor, *, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       bias: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                       tokens: torch.Tensor | None = None, tok_len: torch.Tensor | None = None,
+                       gen_start: torch.Tensor | None = None, repetition: torch.Tensor | None = None,
+                       presence: torch.Tensor | None = None, frequency: torch.Tensor | None = None,
+                       tau: torch.Tensor | None = None, out_lse: torch.Tensor | None = None) -> torch.Tensor:
+        """rlt_process_logits: penalties over the history tokens int32 [B, n] (any strides; tok_len
+        valid ones each, those from gen_start on generated), bias float32 [B or 1, V], mask int32
+        [B or 1, ceil(V / 32)] of allowed bits, per-row float32 parameters; returns out, the
+        log-probabilities that sample() draws from.  With lse, logits are log-probabilities at
+        temperature 1.  out may be logits."""
+        B, V = logits.shape[0], self.cfg.V
+        dev = self.device
+        _need(logits, "logits", torch.float32, dev, (B, V))
+        out = torch.empty((B, V), dtype=torch.float32, device=dev) if out is None else out
+        _need(out, "out", torch.float32, dev, (B, V))
+        a = LogitsArgs()
+
+        def rows(t, what, dtype, n):
+            if t.shape[0] != 1:
+                _need(t, what, dtype, dev, (B, n))
+            else:
+                _need(t, what, dtype, dev, (1, n))
+            if t.stride(1) != 1 and n > 1:
+                raise ValueError(f"{what}: rows must be contiguous")
+            return t.stride(0) if t.shape[0] > 1 else (0 if what in ("bias", "mask") else n)
+
+        a.x, a.x_stride = logits.data_ptr(), rows(logits, "logits", torch.float32, V)
+        a.out, a.out_stride = out.data_ptr(), rows(out, "out", torch.float32, V)
+        if bias is not None:
+            a.bias, a.bias_stride = bias.data_ptr(), rows(bias, "bias", torch.float32, V)
+        if mask is not None:
+            a.mask, a.mask_stride = mask.data_ptr(), rows(mask, "mask", torch.int32, (V + 31) // 32)
+        if tokens is not None:
+            _need(tokens, "tokens", torch.int32, dev, (B, None))
+            a.tokens, a.n_tokens = tokens.data_ptr(), tokens.shape[1]
+            a.seq_stride, a.tok_stride = tokens.stride()
+        elif tok_len is not None or gen_start is not None:
+            raise ValueError("tok_len and gen_start belong to tokens")
+        for name, t, dtype in (("lse", lse, torch.float32), ("tok_len", tok_len, torch.int32),
+                               ("gen_start", gen_start, torch.int32), ("repetition", repetition, torch.float32),
+                               ("presence", presence, torch.float32), ("frequency", frequency, torch.float32),
+                               ("tau", tau, torch.float32), ("out_lse", out_lse, torch.float32)):
+            if t is not None:
+                _need(t, name, dtype, dev, (B,))
+                if not t.is_contiguous():
+                    raise ValueError(f"{name}: must be contiguous")
+                setattr(a, name, t.data_ptr())
+        _check(lib().rlt_process_logits(self.handle, ctypes.byref(a), B, _stream()), "rlt_process_logits")
+        return out
+
     def generate(self, prompt: torch.Tensor, n_new: int, uniforms: torch.Tensor, tau: float = 1.0, top_k: int = 0,
-                 top_p: float = 1.0):
+                 top_p: float = 1.0, *, repetition=None, presence=None, frequency=None,
+                 bias: torch.Tensor | None = None, mask=None):
         """Sample n_new tokens after each prompt row (all rows in lockstep): encode the prompt with a
         cache, step the decoder through it, then repeat [sample x_{t+1} from logp_t, encode it
         incrementally, step].  uniforms: float device [n_new, B].  Returns (tokens [B, P + n_new]
         int32, behaviour log-probs [B, n_new], prompt log-probs [B, P - 1] (entry t-1 = log p of
         x_{t+1}), the state after all P + n_new tokens).  Every step of the loop runs in the
-        library's kernels; nothing is copied to the host."""
+        library's kernels; nothing is copied to the host.
+
+        With any of repetition, presence, frequency (numbers, or float32 device vectors [B]), bias
+        (float32 [B or 1, V]) and mask (int32 [B or 1, ceil(V / 32)], or a function of the number of
+        tokens generated so far and the tokens [B, t] that returns one) each draw is from the logits
+        that process_logits makes of them: the prompt counts for repetition only."""
         prompt = prompt.to(device=self.device, dtype=torch.int32).contiguous()
         B, P = prompt.shape
         T = P + n_new
@@ -354,11 +577,25 @@ class RLTModel:
         blp = torch.empty((n_new, B), dtype=torch.float32, device=self.device)
         lp_prompt = torch.zeros((max(P - 1, 0), B), dtype=torch.float32, device=self.device)
         row = torch.empty((B, self.cfg.V), dtype=torch.float32, device=self.device)
+        control = None
+        if any(x is not None for x in (repetition, presence, frequency, bias, mask)):
+            def vector(x):
+                return x if x is None or isinstance(x, torch.Tensor) else \
+                    torch.full((B,), float(x), dtype=torch.float32, device=self.device)
+            control = dict(repetition=vector(repetition), presence=vector(presence), frequency=vector(frequency),
+                           tau=vector(tau), bias=bias, gen_start=torch.full((B,), P, dtype=torch.int32,
+                                                                            device=self.device))
+            lse = torch.empty(B, dtype=torch.float32, device=self.device)
         for t in range(1, T):                      # step t consumes x_t and predicts x_{t+1}
             if t < P:
                 self.decode_step(st, e, M, next_tok=toks[t], tau=tau, logp_tok=lp_prompt[t - 1])
                 continue
-            self.decode_step(st, e, M, tau=tau, logp_full=row)
+            if control is None:
+                self.decode_step(st, e, M, tau=tau, logp_full=row)
+            else:
+                self.decode_step(st, e, M, tau=1.0, lse=lse, logp_full=row)
+                allowed = mask(t - P, toks[:t].t()) if callable(mask) else mask
+                self.process_logits(row, out=row, lse=lse, mask=allowed, tokens=toks[:t].t(), **control)
             self.sample(row, uniforms[t - P], top_k, top_p, out=toks[t], behaviour_logp=blp[t - P])
             self.encode_append(toks[t], t, cache, T, e, M)
         self.decode_step(st, e, M, tau=tau)         # the transition of x_T

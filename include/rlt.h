@@ -186,6 +186,137 @@ rlt_status rlt_encode_append(rlt_model* m, const int32_t* tokens, int tok_stride
 rlt_status rlt_sample(rlt_model* m, const float* logp, int B, const float* u, int top_k, float top_p,
                       int32_t* tokens, int tok_stride, float* behaviour_logp, void* stream);
 
+/* ---------------------------------------------------------------- paged key/value cache */
+
+/* A ragged batch of new tokens over a paged key/value cache (no counterpart on the pages: the
+ * memory manager of a serving process).  The cache of one layer is a pool
+ *   [n_pages, 2, n_kv_heads, page_size, head_dim]   (plane 0 keys, plane 1 values)
+ * in the model's dtype and head_dim; token p of sequence b lies in page
+ * table[b * table_stride + p / page_size], slot p % page_size.  The N rows of a call are the new
+ * tokens of its B sequences one after another: rows q_start[b] .. q_start[b+1] - 1 are the last
+ * tokens of the kv_len[b] that sequence b has with them, so row q_start[b] + i is at position
+ * kv_len[b] - (q_start[b+1] - q_start[b]) + i.  Sequences without new tokens are allowed, and so
+ * are rows behind the last sequence (q_start[B] < N): they and their outputs are left alone.
+ * Sequences may share pages that none of them writes.
+ * The host needs bounds only, so that a captured call can be replayed with other lengths:
+ * max_q and max_kv bound every sequence's new tokens and kv_len.
+ * What the device finds outside these bounds (lengths beyond max_q, max_kv or N, decreasing
+ * starts, kv_len below the number of new tokens) or in a table entry outside [0, n_pages) latches
+ * RLT_EDEVICE: such a sequence is left out; a key behind such an entry reads page 0 and an append
+ * to one is dropped.  Values (and keys) in slots at and behind kv_len are never used, whatever
+ * they hold; those of a sequence's own tokens must be finite. */
+typedef struct {
+    int32_t B;                  /* sequences, >= 1                                             */
+    int32_t N;                  /* packed rows, >= 1                                           */
+    int32_t max_q;              /* 1 <= max_q <= N                                             */
+    int32_t max_kv;             /* max_q <= max_kv <= min(max_pos, table_stride * page_size)   */
+    const int32_t* q_start;     /* device [B + 1]                                              */
+    const int32_t* kv_len;      /* device [B]                                                  */
+    const int32_t* table;       /* device [B, table_stride]                                    */
+    int32_t table_stride;
+    int32_t page_size;          /* 16, 32, 64, 128 or 256                                      */
+    int32_t n_pages;
+    int32_t n_kv_heads;
+} rlt_paged_batch;
+
+/* Bytes of the pool of one layer. */
+size_t rlt_page_pool_bytes(const rlt_model* m, int n_pages, int page_size, int n_kv_heads);
+
+/* Append the batch's new tokens to the pool: keys after the rotary embedding at their positions
+ * (the model's table), values as they are, both rounded once to the model's dtype.  With q the
+ * rotated queries, rounded alike, go to q_out.
+ *   k, v        device rows [N, n_kv_heads, head_dim], k_stride / v_stride elements apart
+ *   q, q_out    device rows [N, n_heads, head_dim] (or both NULL); q_out has the model's dtype
+ *   src_dtype   of k, v and q: RLT_F32, or RLT_BF16 in a bf16 model
+ * Pointers 16-byte aligned, strides multiples of 8 and at least a row long.  A row's heads are
+ * contiguous; q, k and v may be column ranges of one projection.  q_out may be q itself (same
+ * type and stride).  One launch.  Errors: RLT_EINVAL, RLT_EUNSUPPORTED (N * n_heads beyond 2^30),
+ * RLT_ECUDA. */
+rlt_status rlt_paged_append(rlt_model* m, const rlt_paged_batch* p, void* pool, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const void* q, int64_t q_stride, int n_heads,
+                            void* q_out, int64_t q_out_stride, int src_dtype, void* stream);
+
+/* Workspace bytes of rlt_paged_attention for a batch with these bounds (the device arrays are not
+ * read; 0: none is needed, and ws may be NULL). */
+size_t rlt_paged_attention_workspace_bytes(const rlt_model* m, const rlt_paged_batch* p, int n_heads);
+
+/* Causal attention of the batch's new tokens over the pool, which holds them already: row r at
+ * position t reads keys 0..t of its sequence,
+ *   out[r, h] = sum_j softmax_j(scale q[r, h] . K[j, h / g]) V[j, h / g],  g = n_heads / n_kv_heads,
+ * with float32 softmax statistics and sums, rounded once to the model's dtype.  (On the tensor
+ * cores the probabilities are rounded to bf16 as the encoder's own attention rounds them.)
+ *   q, out      device rows [N, n_heads, head_dim] of the model's dtype (queries after the rotary
+ *               embedding), q_stride / out_stride elements apart; 16-byte aligned, strides
+ *               multiples of 8 and at least a row long
+ *   scale       of the scores, finite and positive; 0: 1 / sqrt(head_dim)
+ *   ws          rlt_paged_attention_workspace_bytes(m, p, n_heads) bytes; calls that may overlap
+ *               on the GPU need workspaces of their own
+ * Errors: RLT_EINVAL, RLT_EUNSUPPORTED (n_heads not a multiple of n_kv_heads, more than 64 query
+ * heads per key head, N * n_heads beyond 2^30), RLT_ECUDA. */
+rlt_status rlt_paged_attention(rlt_model* m, const rlt_paged_batch* p, const void* pool, const void* q,
+                               int64_t q_stride, int n_heads, void* out, int64_t out_stride, float scale, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* Workspace bytes of rlt_encode_chunk. */
+size_t rlt_encode_chunk_workspace_bytes(const rlt_model* m, const rlt_paged_batch* p);
+
+/* Encode the batch's new tokens over a paged encoder cache (deepsonar teardown, 2.5: one execution
+ * semantics for prefill, generation and replay): a prompt, the next turn of a conversation and a
+ * single generated token alike, ragged over the batch.  Every layer appends its keys and values
+ * and attends over the cache; the new encoder outputs go to e[b, t] and their memory projections
+ * to M[..., b, .., t, :] (layouts of rlt_encode, row capacity T_alloc), from where decoder steps
+ * read them.  Equals the token-parallel encoding of the whole sequences up to summation order.
+ *   tokens      device int32 [N]
+ *   pools       L_E pools one after another, each rlt_page_pool_bytes(m, n_pages, page_size, n_heads) bytes
+ * p->n_kv_heads must be the model's n_heads.  Requires max_kv <= T_alloc <= max_pos.  Out-of-range ids latch
+ * RLT_EDEVICE, those of rows behind the last sequence too.  Errors: RLT_EINVAL, RLT_EUNSUPPORTED, RLT_ECUDA. */
+rlt_status rlt_encode_chunk(rlt_model* m, const rlt_paged_batch* p, const int32_t* tokens, void* pools, void* e,
+                            void* M, int T_alloc, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- logits before a draw */
+
+/* Penalties for repeated tokens, a bias, a grammar's mask and the temperature, and the log-softmax
+ * that rlt_sample reads (the behaviour log-probability is then taken under the distribution that
+ * was really sampled from).  Per row b, over the model's V tokens and in float32:
+ *   z = x + lse[b]                               (lse NULL: z = x)
+ *   z = z > 0 ? z / repetition : z * repetition  where the token occurs in the row's history
+ *   z -= presence [c > 0] + frequency * c        c: its occurrences from gen_start on
+ *   z += bias;  z = -inf where the mask's bit is 0;  z /= tau
+ *   out = z - log sum exp z
+ * NULL stands for no lse, bias, mask or history, and for penalties of 1, 0, 0 and a temperature of
+ * 1.  Masked elements count for nothing whatever x holds there. */
+typedef struct {
+    const float* x;             /* device [B, V]: logits, or log-probabilities at temperature 1 with
+                                 * lse their log-sum-exp (logp_full and lse of rlt_decode_step)  */
+    int64_t x_stride;           /* elements between rows, >= V                                   */
+    float* out;                 /* device [B, V], may be x                                       */
+    int64_t out_stride;
+    const float* lse;           /* device [B] or NULL                                            */
+    const float* bias;          /* device [B, V] or NULL                                         */
+    int64_t bias_stride;        /* >= V, or 0: one row for the whole batch                       */
+    const uint32_t* mask;       /* device [B, ceil(V / 32)] or NULL: bit v % 32 of word v / 32 is
+                                 * 1 where token v is allowed                                    */
+    int64_t mask_stride;        /* >= ceil(V / 32), or 0: one row for the whole batch            */
+    const int32_t* tokens;      /* device, or NULL: token i of row b's history is at
+                                 * tokens[b * seq_stride + i * tok_stride]                       */
+    int64_t seq_stride, tok_stride;
+    int32_t n_tokens;           /* largest history, >= 0                                         */
+    const int32_t* tok_len;     /* device [B]: the rows' histories, or NULL: n_tokens each       */
+    const int32_t* gen_start;   /* device [B]: where the prompt ends, or NULL: 0                 */
+    const float* repetition;    /* device [B] or NULL, each of the four; > 0                     */
+    const float* presence;
+    const float* frequency;
+    const float* tau;           /* > 0                                                           */
+    float* out_lse;             /* device [B] or NULL: log sum exp z                             */
+} rlt_logits;
+
+/* One launch; vectors of 16 bytes where x, out and bias are 16-byte aligned with strides that are
+ * multiples of 4.  A row that the mask leaves without a token becomes -inf throughout and latches
+ * RLT_EDEVICE, as do history ids outside [0, V) (skipped), lengths outside [0, n_tokens] (clamped)
+ * and a repetition or tau that is not above 0 (taken as 1).
+ * Errors: RLT_EINVAL, RLT_EUNSUPPORTED (V above 262144), RLT_ECUDA. */
+rlt_status rlt_process_logits(rlt_model* m, const rlt_logits* a, int B, void* stream);
+
 /* ---------------------------------------------------------------- decoder state */
 
 /* Bytes of one decoder state H for B sequences: a 256-byte header, s [B, d] float32, the SWA
