@@ -194,6 +194,243 @@ __global__ void __launch_bounds__(128) k_paged_simt(PagedArgs p, PagedAttnArgs a
     }
 }
 
+// ------------------------------------------------------------------ few rows, tensor cores
+// 16 rows of one key head against groups of 16 keys that the warps take in turn, on
+// mma.m16n8k16, keys and values straight from memory to the fragments.  What bounds it is
+// reading the keys and values once; a tile's 16 rows are mostly empty in a decode step, and the
+// warp-level product needs no staging, no tensor memory and no barrier on the way.
+//
+// The contraction over head_dim may run in any order, so lane t of a quad takes 8 consecutive
+// elements of its key (one 16-byte load) and the queries are loaded to match; columns of the
+// output are dealt so that a lane reads 16 consecutive bytes of a value and ends up with
+// consecutive output columns.
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// W consecutive 32-bit words (zeros where ok is false)
+template <int W>
+__device__ __forceinline__ void load_words(const bf16* p, bool ok, uint32_t* r) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) r[i] = 0;
+    if (!ok) return;
+    if (W == 1) r[0] = *reinterpret_cast<const uint32_t*>(p);
+    if (W == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        r[0] = x.x; r[W > 1 ? 1 : 0] = x.y;
+    }
+    if (W == 4) {
+        const uint4 x = ld16(p);
+        r[0] = x.x; r[W > 1 ? 1 : 0] = x.y; r[W > 2 ? 2 : 0] = x.z; r[W > 2 ? 3 : 0] = x.w;
+    }
+}
+
+constexpr int MMA_WARPS = 4;
+template <int HD>
+struct MmaShape {
+    static constexpr int QW = HD >= 32 ? 4 : 2;             // words per lane and piece of a key
+    static constexpr int QP = HD >= 32 ? HD / 32 : 1;       // pieces
+    static constexpr int VW = HD >= 64 ? 4 : HD / 16;       // words per lane and piece of a value
+    static constexpr int VP = HD >= 64 ? HD / 64 : 1;
+    static constexpr int NT = HD / 8;                       // output tiles of 8 columns
+    static constexpr int LD = HD + 4;
+    static constexpr int SMEM = MMA_WARPS * 16 * LD * 4;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(MMA_WARPS * 32) k_paged_mma(PagedArgs p, PagedAttnArgs a, UnitPlan u) {
+    using S = MmaShape<HD>;
+    extern __shared__ __align__(16) float sm[];             // [warps][16][LD]: accumulators, maximum, sum
+    pdl_wait();
+    pdl_trigger();
+    Unit w;
+    if (!find_unit(p, u, blockIdx.x, false, w)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int row0 = w.tile * 16, rows = min(16, w.s.nq * u.g - row0), ctx = w.s.kv - w.s.nq;
+    const int last = ctx + (row0 + rows - 1) / u.g;
+    const int k_begin = w.split * w.chunk, k_end = min(last + 1, k_begin + w.chunk);
+    if (k_begin >= k_end) return;
+    const float c2 = a.scale * LOG2E;
+
+    uint32_t q[2][S::QP][S::QW];
+    int limit[2];                                           // the last key of rows g and g + 8
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = row0 + g + 8 * i, tok = row / u.g;
+        const bool ok = g + 8 * i < rows;
+        limit[i] = ok ? ctx + tok : -1;
+        const bf16* qp = reinterpret_cast<const bf16*>(a.q) + (long long)(w.s.q0 + tok) * a.q_stride +
+                         (long long)(w.head * u.g + row % u.g) * HD;
+#pragma unroll
+        for (int c = 0; c < S::QP; ++c) load_words<S::QW>(qp + (c * 4 + t) * S::QW * 2, ok, q[i][c]);
+    }
+
+    float m[2] = {NEG_BIG, NEG_BIG}, l[2] = {0.f, 0.f};     // m of the scores as they are
+    float o[S::NT][4];
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+
+    const bf16* pool = reinterpret_cast<const bf16*>(a.pool);
+    const long long head_elems = (long long)HD << p.page_shift, v_off = p.Hkv * head_elems;
+    const int page_mask = (1 << p.page_shift) - 1;
+    // this warp's groups: keys k_begin + 16 (warp + 4 i); lane j keeps the page of group i0 + j
+    const int n_groups = (k_end - k_begin + 15) / 16;
+    const int mine = n_groups > warp ? (n_groups - warp + MMA_WARPS - 1) / MMA_WARPS : 0;
+    auto key0 = [&](int i) { return k_begin + 16 * (warp + MMA_WARPS * i); };
+    int pages = 0;
+    auto load_pages = [&](int i0) {
+        const int i = i0 + lane;
+        pages = i < mine ? max(load_page(p, w.b, key0(i)), 0) : 0;
+    };
+    auto base = [&](int i) {
+        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+        return pool + ((long long)page * 2 * p.Hkv + w.head) * head_elems + (long long)(key0(i) & page_mask) * HD;
+    };
+    uint32_t kf[2][S::QP][S::QW], vf[4][S::VP][S::VW];
+    auto load_k = [&](const bf16* kp, int i) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int c = 0; c < S::QP; ++c)
+                load_words<S::QW>(kp + (long long)(8 * n + g) * HD + (c * 4 + t) * S::QW * 2, key0(i) + 8 * n + g < k_end,
+                                  kf[n][c]);
+    };
+    auto load_v = [&](const bf16* vp, int i) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int j = 2 * t + (n & 1) + 8 * (n >> 1);   // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+            for (int c = 0; c < S::VP; ++c)
+                load_words<S::VW>(vp + (long long)j * HD + (c * 8 + g) * S::VW * 2, key0(i) + j < k_end, vf[n][c]);
+        }
+    };
+
+    if (mine > 0) {
+        load_pages(0);
+        const bf16* kp = base(0);
+        load_k(kp, 0);
+        load_v(kp + v_off, 0);
+    }
+    for (int i = 0; i < mine; ++i) {
+        float s[2][4] = {};
+#pragma unroll
+        for (int c = 0; c < S::QP; ++c)
+#pragma unroll
+            for (int h = 0; h < S::QW; h += 2) {
+                const uint32_t af[4] = {q[0][c][h], q[1][c][h], q[0][c][h + 1], q[1][c][h + 1]};
+#pragma unroll
+                for (int n = 0; n < 2; ++n) mma16816(s[n], af, kf[n][c][h], kf[n][c][h + 1]);
+            }
+        // the next group's keys are under way while this one's softmax runs
+        const bf16* kp = nullptr;
+        if (i + 1 < mine) {
+            if (((i + 1) & 31) == 0) load_pages(i + 1);
+            kp = base(i + 1);
+            load_k(kp, i + 1);
+        }
+        const int k0 = key0(i);
+        float mx[2] = {m[0], m[1]};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (k0 + 8 * n + 2 * t + (e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
+                mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float al = ex2_approx((m[r] - mx[r]) * c2);
+                l[r] *= al;
+                m[r] = mx[r];
+#pragma unroll
+                for (int j = 0; j < S::NT; ++j) { o[j][2 * r] *= al; o[j][2 * r + 1] *= al; }
+            }
+        }
+        // probabilities rounded to bf16 for the product; the sum is of the rounded values, so that
+        // the result stays a weighted mean of the values
+        uint32_t pf[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float mc = m[r] == NEG_BIG ? 0.f : m[r] * c2;
+                __nv_bfloat162 h = __floats2bfloat162_rn(ex2_approx(fmaf(s[n][2 * r], c2, -mc)),
+                                                         ex2_approx(fmaf(s[n][2 * r + 1], c2, -mc)));
+                const uint32_t x = *reinterpret_cast<uint32_t*>(&h);
+                l[r] += __uint_as_float(x << 16) + __uint_as_float(x & 0xffff0000u);
+                pf[2 * n + r] = x;
+            }
+#pragma unroll
+        for (int c = 0; c < S::VP; ++c)
+#pragma unroll
+            for (int e = 0; e < S::VW; ++e) {
+                mma16816(o[(c * S::VW + e) * 2], pf, __byte_perm(vf[0][c][e], vf[1][c][e], 0x5410),
+                         __byte_perm(vf[2][c][e], vf[3][c][e], 0x5410));
+                mma16816(o[(c * S::VW + e) * 2 + 1], pf, __byte_perm(vf[0][c][e], vf[1][c][e], 0x7632),
+                         __byte_perm(vf[2][c][e], vf[3][c][e], 0x7632));
+            }
+        if (i + 1 < mine) load_v(kp + v_off, i + 1);
+    }
+
+    // Join the warps.  Lane t of quad g has, of piece c, columns (c * 8 + 2t) * 2 VW .. + 4 VW - 1:
+    // tile j's element 0 is column (c * 8 + 2t) * 2 VW + j, element 1 is 2 VW further.
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        float* dst = sm + (warp * 16 + g + 8 * r) * S::LD;
+        if (g + 8 * r < rows) {
+#pragma unroll
+            for (int c = 0; c < S::VP; ++c)
+#pragma unroll
+                for (int e = 0; e < 2 * S::VW; ++e) {
+                    dst[(c * 8 + 2 * t) * 2 * S::VW + e] = o[c * S::VW * 2 + e][2 * r];
+                    dst[(c * 8 + 2 * t + 1) * 2 * S::VW + e] = o[c * S::VW * 2 + e][2 * r + 1];
+                }
+            if (t == 0) { dst[HD] = m[r] * c2; dst[HD + 1] = l[r]; }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * HD; i += MMA_WARPS * 32) {
+        const int r = i / HD, col = i % HD;
+        float mt = NEG_BIG;
+#pragma unroll
+        for (int x = 0; x < MMA_WARPS; ++x) mt = fmaxf(mt, sm[(x * 16 + r) * S::LD + HD]);
+        float lt = 0.f, acc = 0.f;
+#pragma unroll
+        for (int x = 0; x < MMA_WARPS; ++x) {
+            const float* src = sm + (x * 16 + r) * S::LD;
+            const float f = ex2_approx(src[HD] - mt);
+            lt += f * src[HD + 1];
+            acc += f * src[col];
+        }
+        if (w.n_splits > 1) {
+            float* pr = part_row(a, u, w.slot, r);
+            pr[col] = acc;
+            if (col == 0) { pr[HD] = mt; pr[HD + 1] = lt; }
+        } else {
+            const int row = row0 + r;
+            reinterpret_cast<bf16*>(a.o)[(long long)(w.s.q0 + row / u.g) * a.o_stride +
+                                         (long long)(w.head * u.g + row % u.g) * HD + col] = from_f<bf16>(acc / lt);
+        }
+    }
+}
+
 // Sequences of any number of rows; 2 rows per unit when no sequence has more, else 16.
 UnitPlan simt_plan(const PagedArgs& p, int H) {
     UnitPlan u;
@@ -208,13 +445,32 @@ UnitPlan simt_plan(const PagedArgs& p, int H) {
     return u;
 }
 
+UnitPlan mma_plan(const PagedArgs& p, int H) {
+    UnitPlan u;
+    u.g = H / p.Hkv;
+    u.rt = 16;
+    u.rows_lo = 1;
+    u.rows_hi = 1 << 30;
+    u.min_chunk = 256;
+    u.chunk_align = 64;
+    u.target = 148 * 12;
+    u.slots = (int)plan_slots(p, u);
+    return u;
+}
+
+template <int HD>
+cudaError_t run_mma(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
+    const long long grid = plan_items(p, u) + (u.slots ? u.target : 0);
+    return launch_k(L, k_paged_mma<HD>, (unsigned)grid, MMA_WARPS * 32, MmaShape<HD>::SMEM, p, a, u);
+}
+
 template <typename T, int HD, int R>
 cudaError_t run_simt(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
     constexpr int RT = 2 * R;
     constexpr size_t smem = (64 * (HD + 4) + 64 * HD + RT * HD + RT * 64 + RT) * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(k_paged_simt<T, HD, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const long long grid = plan_items(p, u) + u.target;
+    const long long grid = plan_items(p, u) + (u.slots ? u.target : 0);
     return launch_k(L, k_paged_simt<T, HD, R>, (unsigned)grid, 128, smem, p, a, u);
 }
 template <typename T, int R>
@@ -238,17 +494,27 @@ cudaError_t join(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const Uni
 }  // namespace
 
 size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16) {
-    const UnitPlan u = simt_plan(p, H);
+    const UnitPlan u = is_bf16 ? mma_plan(p, H) : simt_plan(p, H);
     return (size_t)u.slots * u.rt * (hd + 2) * sizeof(float);
 }
 
-template <typename T>
-cudaError_t launch_paged_attention(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
+template <>
+cudaError_t launch_paged_attention<float>(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
     const UnitPlan u = simt_plan(p, a.H);
-    cudaError_t e = u.rt == 2 ? run_simt_hd<T, 1>(L, p, a, u) : run_simt_hd<T, 8>(L, p, a, u);
-    return e == cudaSuccess ? join<T>(L, p, a, u) : e;
+    cudaError_t e = u.rt == 2 ? run_simt_hd<float, 1>(L, p, a, u) : run_simt_hd<float, 8>(L, p, a, u);
+    return e == cudaSuccess ? join<float>(L, p, a, u) : e;
 }
-template cudaError_t launch_paged_attention<float>(Launch, const PagedArgs&, const PagedAttnArgs&);
-template cudaError_t launch_paged_attention<bf16>(Launch, const PagedArgs&, const PagedAttnArgs&);
+template <>
+cudaError_t launch_paged_attention<bf16>(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
+    const UnitPlan u = mma_plan(p, a.H);
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (a.hd) {
+        case 16: e = run_mma<16>(L, p, a, u); break;
+        case 32: e = run_mma<32>(L, p, a, u); break;
+        case 64: e = run_mma<64>(L, p, a, u); break;
+        case 128: e = run_mma<128>(L, p, a, u); break;
+    }
+    return e == cudaSuccess ? join<bf16>(L, p, a, u) : e;
+}
 
 }  // namespace rlt
