@@ -79,6 +79,7 @@ struct UnitPlan {
     int chunk_align;
     int target;
     int slots;                  // partial states that the workspace holds
+    long long part;             // the first of them, in floats
 };
 
 struct Unit {
@@ -205,9 +206,17 @@ struct PagedAttnArgs {
     float scale;
     float* part;                // partial states of cut items
 };
+// A row of a cut item's partial state: head_dim accumulators (not divided by the sum), the maximum
+// (of base-2 scaled scores) and the sum.
+__device__ __forceinline__ float* part_row(const PagedAttnArgs& a, const UnitPlan& u, int slot, int row, int hd) {
+    return a.part + u.part + ((long long)slot * u.rt + row) * (hd + 2);
+}
 size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16);
 template <typename T>
 cudaError_t launch_paged_attention(Launch L, const PagedArgs& p, const PagedAttnArgs& a);
+
+// ------------------------------------------------------------------ paged_attn_tc.cu
+cudaError_t launch_paged_tc(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u);
 
 // ------------------------------------------------------------------ logits.cu
 struct LogitsArgs {

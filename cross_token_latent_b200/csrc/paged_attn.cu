@@ -13,36 +13,33 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NEG_BIG = -1e30f;
 
-// Where a unit's results go: the output when its item is not cut, else a slot of partial states,
-// per row head_dim accumulators (not divided by the sum), the maximum (of scaled base-2 scores)
-// and the sum.
-__device__ __forceinline__ float* part_row(const PagedAttnArgs& a, const UnitPlan& u, int slot, int row) {
-    return a.part + ((long long)slot * u.rt + row) * (a.hd + 2);
-}
-
-// Joins the partial states of one cut item (block: one item, warps over its rows).
+// Joins the partial states of the cut items: a block takes 16 rows of one item, its warps row by
+// row.  The batch may have been cut by two plans (few rows, many rows); the first n1 blocks of x
+// are the first one's items.
+constexpr int JOIN_ROWS = 16;
 template <typename T>
-__global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u) {
+__global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u1, UnitPlan u2, int n1) {
     // The kernel in front waited for its predecessor before it let this one start, so the batch's
     // lengths may be read here; the partial states only behind the wait.
+    const UnitPlan& u = (int)blockIdx.x < n1 ? u1 : u2;
+    const int row_begin = blockIdx.y * JOIN_ROWS;
     Unit w;
-    const bool any = find_unit(p, u, blockIdx.x, true, w);
+    const bool any = row_begin < u.rt && find_unit(p, u, (int)blockIdx.x < n1 ? blockIdx.x : blockIdx.x - n1, true, w);
     pdl_wait();
     pdl_trigger();
     if (!any) return;
     const int lane = threadIdx.x & 31, rows = w.s.nq * u.g;
-    const int q = threadIdx.x >> 5;
-    for (int i = q; i < u.rt; i += 4) {
+    for (int i = row_begin + (threadIdx.x >> 5); i < min(row_begin + JOIN_ROWS, u.rt); i += 4) {
         const int row = w.tile * u.rt + i;
         if (row >= rows) break;
         const int tok = row / u.g, keys = w.s.kv - w.s.nq + tok + 1;
         const int n = min(w.n_splits, (keys + w.chunk - 1) / w.chunk);     // units that saw a key of this row
         float m = NEG_BIG;
-        for (int j = lane; j < n; j += 32) m = fmaxf(m, part_row(a, u, w.slot + j, i)[a.hd]);
+        for (int j = lane; j < n; j += 32) m = fmaxf(m, part_row(a, u, w.slot + j, i, a.hd)[a.hd]);
         m = warp_max(m);
         float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j = 0; j < n; ++j) {
-            const float* r = part_row(a, u, w.slot + j, i);
+            const float* r = part_row(a, u, w.slot + j, i, a.hd);
             const float f = exp2f(r[a.hd] - m);
             l += f * r[a.hd + 1];
 #pragma unroll
@@ -181,7 +178,7 @@ __global__ void __launch_bounds__(128) k_paged_simt(PagedArgs p, PagedAttnArgs a
             const int r = grp * RPG + i, row = row0 + r;
             if (r < rows) {
                 if (w.n_splits > 1) {
-                    float* pr = part_row(a, u, w.slot, r);
+                    float* pr = part_row(a, u, w.slot, r, HD);
                     pr[col] = acc[i];
                     if (col == 0) { pr[HD] = Mx[r]; pr[HD + 1] = Al[r]; }
                 } else {
@@ -420,7 +417,7 @@ __global__ void __launch_bounds__(MMA_WARPS * 32) k_paged_mma(PagedArgs p, Paged
             acc += f * src[col];
         }
         if (w.n_splits > 1) {
-            float* pr = part_row(a, u, w.slot, r);
+            float* pr = part_row(a, u, w.slot, r, HD);
             pr[col] = acc;
             if (col == 0) { pr[HD] = mt; pr[HD + 1] = lt; }
         } else {
@@ -431,36 +428,50 @@ __global__ void __launch_bounds__(MMA_WARPS * 32) k_paged_mma(PagedArgs p, Paged
     }
 }
 
-// Sequences of any number of rows; 2 rows per unit when no sequence has more, else 16.
-UnitPlan simt_plan(const PagedArgs& p, int H) {
+UnitPlan make_plan(const PagedArgs& p, int H, int rt, int rows_lo, int rows_hi, int min_chunk, int align, int target) {
     UnitPlan u;
     u.g = H / p.Hkv;
-    u.rt = (long long)p.max_q * u.g <= 2 ? 2 : 16;
-    u.rows_lo = 1;
-    u.rows_hi = 1 << 30;
-    u.min_chunk = 256;
-    u.chunk_align = 64;
-    u.target = 148 * 8;
+    u.rt = rt;
+    u.rows_lo = rows_lo;
+    u.rows_hi = rows_hi;
+    u.min_chunk = min_chunk;
+    u.chunk_align = align;
+    u.target = target;
     u.slots = (int)plan_slots(p, u);
+    u.part = 0;
     return u;
 }
+constexpr int ANY = 1 << 30;
+// Float32: 2 rows per unit when no sequence has more, else 16.
+UnitPlan simt_plan(const PagedArgs& p, int H) {
+    return make_plan(p, H, (long long)p.max_q * (H / p.Hkv) <= 2 ? 2 : 16, 1, ANY, 256, 64, 148 * 8);
+}
 
-UnitPlan mma_plan(const PagedArgs& p, int H) {
-    UnitPlan u;
-    u.g = H / p.Hkv;
-    u.rt = 16;
-    u.rows_lo = 1;
-    u.rows_hi = 1 << 30;
-    u.min_chunk = 256;
-    u.chunk_align = 64;
-    u.target = 148 * 12;
-    u.slots = (int)plan_slots(p, u);
-    return u;
+// bf16: sequences of at most `few` rows per key head go to the warp-level kernel, those of more to
+// the tcgen05 kernel, which head widths of 64 and 128 have (and pools whose rows TMA can count).
+constexpr int FEW_ROWS = 16;
+struct Bf16Plans {
+    bool tc;
+    UnitPlan u_mma, u_tc;
+};
+Bf16Plans bf16_plans(const PagedArgs& p, int H, int hd) {
+    Bf16Plans b;
+    const int g = H / p.Hkv;
+    b.tc = hd >= 64 && (long long)p.max_q * g > FEW_ROWS &&
+           (((long long)p.n_pages * 2 * p.Hkv) << p.page_shift) < (1LL << 31);
+    PagedArgs few = p;              // its bounds
+    if (b.tc) few.max_q = FEW_ROWS / g < 1 ? 1 : FEW_ROWS / g;
+    b.u_mma = make_plan(few, H, 16, 1, b.tc ? FEW_ROWS : ANY, 256, 64, 148 * 12);
+    if (b.tc) {
+        b.u_tc = make_plan(p, H, 128 / g * g * 2, FEW_ROWS + 1, ANY, 512, 128, 148 * 2);
+        b.u_tc.part = (long long)b.u_mma.slots * b.u_mma.rt * (hd + 2);
+    }
+    return b;
 }
 
 template <int HD>
-cudaError_t run_mma(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
-    const long long grid = plan_items(p, u) + (u.slots ? u.target : 0);
+cudaError_t run_mma(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u, long long items) {
+    const long long grid = items + (u.slots ? u.target : 0);
     return launch_k(L, k_paged_mma<HD>, (unsigned)grid, MMA_WARPS * 32, MmaShape<HD>::SMEM, p, a, u);
 }
 
@@ -484,37 +495,52 @@ cudaError_t run_simt_hd(Launch L, const PagedArgs& p, const PagedAttnArgs& a, co
     return cudaErrorInvalidValue;
 }
 
-template <typename T>
-cudaError_t join(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
-    if (u.slots == 0) return cudaSuccess;
-    const long long items = plan_items(p, u);           // at most one cut item per two slots
-    return launch_k(L, k_paged_join<T>, (unsigned)(items < u.target ? items : u.target), 128, 0, p, a, u);
+// At most one cut item per two slots, `target` of them, and no more than there are items.
+int join_items(const UnitPlan& u, long long items) {
+    const long long n = items < u.target ? items : u.target;
+    return u.slots == 0 ? 0 : (int)n;
 }
 
 }  // namespace
 
 size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16) {
-    const UnitPlan u = is_bf16 ? mma_plan(p, H) : simt_plan(p, H);
-    return (size_t)u.slots * u.rt * (hd + 2) * sizeof(float);
+    if (!is_bf16) {
+        const UnitPlan u = simt_plan(p, H);
+        return (size_t)u.slots * u.rt * (hd + 2) * sizeof(float);
+    }
+    const Bf16Plans b = bf16_plans(p, H, hd);
+    size_t n = (size_t)b.u_mma.slots * b.u_mma.rt;
+    if (b.tc) n += (size_t)b.u_tc.slots * b.u_tc.rt;
+    return n * (hd + 2) * sizeof(float);
 }
 
 template <>
 cudaError_t launch_paged_attention<float>(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
     const UnitPlan u = simt_plan(p, a.H);
     cudaError_t e = u.rt == 2 ? run_simt_hd<float, 1>(L, p, a, u) : run_simt_hd<float, 8>(L, p, a, u);
-    return e == cudaSuccess ? join<float>(L, p, a, u) : e;
+    const int n = join_items(u, plan_items(p, u));
+    if (e != cudaSuccess || n == 0) return e;
+    return launch_k(L, k_paged_join<float>, dim3(n, (u.rt + JOIN_ROWS - 1) / JOIN_ROWS), 128, 0, p, a, u, u, n);
 }
 template <>
 cudaError_t launch_paged_attention<bf16>(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
-    const UnitPlan u = mma_plan(p, a.H);
+    const Bf16Plans b = bf16_plans(p, a.H, a.hd);
+    // every sequence of few rows is one tile
+    const long long mma_items = b.tc ? (long long)p.B * p.Hkv : plan_items(p, b.u_mma);
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.hd) {
-        case 16: e = run_mma<16>(L, p, a, u); break;
-        case 32: e = run_mma<32>(L, p, a, u); break;
-        case 64: e = run_mma<64>(L, p, a, u); break;
-        case 128: e = run_mma<128>(L, p, a, u); break;
+        case 16: e = run_mma<16>(L, p, a, b.u_mma, mma_items); break;
+        case 32: e = run_mma<32>(L, p, a, b.u_mma, mma_items); break;
+        case 64: e = run_mma<64>(L, p, a, b.u_mma, mma_items); break;
+        case 128: e = run_mma<128>(L, p, a, b.u_mma, mma_items); break;
     }
-    return e == cudaSuccess ? join<bf16>(L, p, a, u) : e;
+    if (e == cudaSuccess && b.tc) e = launch_paged_tc(L, p, a, b.u_tc);
+    if (e != cudaSuccess) return e;
+    const int n1 = join_items(b.u_mma, mma_items), n2 = b.tc ? join_items(b.u_tc, plan_items(p, b.u_tc)) : 0;
+    if (n1 + n2 == 0) return e;
+    const int rt = n2 ? b.u_tc.rt : b.u_mma.rt;
+    return launch_k(L, k_paged_join<bf16>, dim3(n1 + n2, (rt + JOIN_ROWS - 1) / JOIN_ROWS), 128, 0, p, a, b.u_mma,
+                    b.tc ? b.u_tc : b.u_mma, n1);
 }
 
 }  // namespace rlt
