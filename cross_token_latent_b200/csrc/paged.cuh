@@ -162,6 +162,144 @@ __device__ __forceinline__ bool find_unit(const PagedArgs& p, const UnitPlan& u,
     return false;
 }
 
+// ------------------------------------------------------------------ shares of attention work
+// The tcgen05 kernel takes its work as one long line of steps (a tile of rows against 128 keys):
+// sequence by sequence, tile by tile, head by head, key by key, cut into equal shares, one per
+// CTA.  A share begins and ends anywhere, so every CTA has the same work whatever the raggedness
+// and the causal order; an item (a tile and head) is cut only where a share ends, which leaves at
+// most two partial states per CTA.  With `whole` an item counts as one step and is never cut.
+constexpr int STEP_KEYS = 128;
+struct SharePlan {
+    int g;                      // query heads per key head
+    int rt, toks;               // rows and tokens per tile: rt = toks * g
+    int rows_lo;                // the kernel takes sequences of at least that many rows
+    int ctas;
+    int whole;
+    long long part;             // partial states, in floats: slots 2c and 2c + 1 are CTA c's
+};
+
+__device__ __forceinline__ int share_tiles(const SharePlan& u, const Seq& s) {
+    return s.nq * u.g >= u.rows_lo ? (s.nq + u.toks - 1) / u.toks : 0;
+}
+// steps of one of the sequence's items: key tiles up to the last key that a row of the tile sees
+__device__ __forceinline__ int share_keys(const SharePlan& u, const Seq& s, int tile) {
+    return s.kv - s.nq + min(s.nq, (tile + 1) * u.toks);
+}
+__device__ __forceinline__ int share_steps(const SharePlan& u, const Seq& s, int tile) {
+    return u.whole ? 1 : (share_keys(u, s, tile) + STEP_KEYS - 1) / STEP_KEYS;
+}
+// Sum over i < n of floor((a i + b) / m), by Euclid's steps.
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+    long long sum = 0;
+    while (n > 0) {
+        sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
+        a %= m;
+        b %= m;
+        const unsigned long long y = (unsigned long long)a * n + b;
+        if (y < m) break;
+        n = (unsigned)(y / m);
+        b = (unsigned)(y % m);
+        const unsigned t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+// steps of all tiles of the sequence, for one head
+__device__ __forceinline__ long long share_seq_steps(const SharePlan& u, const Seq& s) {
+    const int tiles = share_tiles(u, s);
+    if (tiles == 0 || u.whole) return tiles;
+    const int full = s.nq / u.toks;
+    long long n = floor_sum(full, STEP_KEYS, u.toks, s.kv - s.nq + u.toks + STEP_KEYS - 1);
+    if (full < tiles) n += (s.kv + STEP_KEYS - 1) / STEP_KEYS;
+    return n;
+}
+
+struct ShareStart {
+    long long total, share;     // steps in all, per CTA
+    int b;                      // the sequence that share number `index` begins in
+    long long off;              // and the step within it (over its heads and tiles)
+};
+struct ShareSmem {
+    long long warp[32];
+    long long off;
+    int b;
+};
+// Where share `index` begins; all threads of the block, false where there is no such share.
+__device__ __forceinline__ bool find_share(const PagedArgs& p, const SharePlan& u, int index, ShareSmem& sm, ShareStart& out) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    long long mine = 0, first = 0;
+    for (int b = tid; b < p.B; b += blockDim.x) {
+        const long long n = share_seq_steps(u, load_seq(p, b)) * p.Hkv;
+        if (b == tid) first = n;
+        mine += n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sm.warp[warp] = mine;
+    if (tid == 0) sm.b = -1;
+    __syncthreads();
+    long long total = 0;
+    for (int i = 0; i < warps; ++i) total += sm.warp[i];
+    // a share of a few steps at least: a CTA costs about two to set up
+    const long long even = (total + u.ctas - 1) / u.ctas, least = u.whole ? 1 : 4;
+    out.total = total;
+    out.share = even > least ? even : least;
+    const long long target = out.share * index;
+    if (target >= total) return false;
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
+        const int b = b0 + tid;
+        const long long n = b0 == 0 ? first : (b < p.B ? share_seq_steps(u, load_seq(p, b)) * p.Hkv : 0);
+        long long end = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += y;
+        }
+        __syncthreads();                    // sm.warp is free
+        if (lane == 31) sm.warp[warp] = end;
+        __syncthreads();
+        long long before = base;
+        for (int i = 0; i < warp; ++i) before += sm.warp[i];
+        if (before + end - n <= target && target < before + end) {
+            sm.b = b;
+            sm.off = target - (before + end - n);
+        }
+        for (int i = 0; i < warps; ++i) base += sm.warp[i];
+        __syncthreads();
+        if (sm.b >= 0) break;
+    }
+    out.b = sm.b;
+    out.off = sm.off;
+    return out.b >= 0;
+}
+// The tile, head and step of step number off of a sequence, found by a whole warp.
+__device__ __forceinline__ void locate_step(const SharePlan& u, const Seq& s, int Hkv, long long off, int& tile, int& head,
+                                            int& step) {
+    const int lane = threadIdx.x & 31, tiles = share_tiles(u, s);
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+        const int n = t0 + lane < tiles ? share_steps(u, s, t0 + lane) : 0;
+        int end = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, off < (long long)end * Hkv);
+        if (hit) {
+            const int src = __ffs(hit) - 1, steps = __shfl_sync(0xffffffffu, n, src);
+            const int rem = (int)(off - (long long)(__shfl_sync(0xffffffffu, end, src) - steps) * Hkv);
+            tile = t0 + src;
+            head = rem / steps;
+            step = rem % steps;
+            return;
+        }
+        off -= (long long)__shfl_sync(0xffffffffu, end, 31) * Hkv;
+    }
+    tile = head = step = 0;
+}
+
 // Bounds that the host knows: items of a plan, and the slots of its partial states.
 inline long long plan_items(const PagedArgs& p, const UnitPlan& u) {
     const long long rows = (long long)p.N * u.g;
@@ -208,7 +346,8 @@ struct PagedAttnArgs {
 };
 // A row of a cut item's partial state: head_dim accumulators (not divided by the sum), the maximum
 // (of base-2 scaled scores) and the sum.
-__device__ __forceinline__ float* part_row(const PagedAttnArgs& a, const UnitPlan& u, int slot, int row, int hd) {
+template <typename Plan>
+__device__ __forceinline__ float* part_row(const PagedAttnArgs& a, const Plan& u, int slot, int row, int hd) {
     return a.part + u.part + ((long long)slot * u.rt + row) * (hd + 2);
 }
 size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16);
@@ -216,7 +355,9 @@ template <typename T>
 cudaError_t launch_paged_attention(Launch L, const PagedArgs& p, const PagedAttnArgs& a);
 
 // ------------------------------------------------------------------ paged_attn_tc.cu
-cudaError_t launch_paged_tc(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u);
+// Row stages of a tile: what the accumulators of 256 TMEM columns allow.
+constexpr int paged_tc_stages(int hd) { return 256 / hd; }
+cudaError_t launch_paged_tc(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const SharePlan& u);
 
 // ------------------------------------------------------------------ logits.cu
 struct LogitsArgs {

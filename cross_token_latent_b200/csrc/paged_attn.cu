@@ -13,44 +13,81 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NEG_BIG = -1e30f;
 
+// One output row of a cut item from n partial states; state j's row is at r(j).
+template <typename T, typename F>
+__device__ __forceinline__ void join_row(T* o, int hd, int n, F r) {
+    const int lane = threadIdx.x & 31;
+    float m = NEG_BIG;
+    for (int j = lane; j < n; j += 32) m = fmaxf(m, r(j)[hd]);
+    m = warp_max(m);
+    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < n; ++j) {
+        const float* x = r(j);
+        const float f = exp2f(x[hd] - m);
+        l += f * x[hd + 1];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (c * 32 + lane < hd) acc[c] += f * x[c * 32 + lane];
+    }
+    const float inv = 1.0f / l;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (c * 32 + lane < hd) o[c * 32 + lane] = from_f<T>(acc[c] * inv);
+}
+
 // Joins the partial states of the cut items: a block takes 16 rows of one item, its warps row by
-// row.  The batch may have been cut by two plans (few rows, many rows); the first n1 blocks of x
-// are the first one's items.
+// row.  The first n1 blocks of x are cut items of the plan u; with the plan us, block n1 + c - 1
+// is the item that share c begins inside of, if share c is the first to.
 constexpr int JOIN_ROWS = 16;
 template <typename T>
-__global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u1, UnitPlan u2, int n1) {
+__global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u, int n1, SharePlan us) {
     // The kernel in front waited for its predecessor before it let this one start, so the batch's
     // lengths may be read here; the partial states only behind the wait.
-    const UnitPlan& u = (int)blockIdx.x < n1 ? u1 : u2;
-    const int row_begin = blockIdx.y * JOIN_ROWS;
-    Unit w;
-    const bool any = row_begin < u.rt && find_unit(p, u, (int)blockIdx.x < n1 ? blockIdx.x : blockIdx.x - n1, true, w);
+    __shared__ ShareSmem sm;
+    const int row_begin = blockIdx.y * JOIN_ROWS, warp = threadIdx.x >> 5;
+    if ((int)blockIdx.x < n1) {
+        Unit w;
+        const bool any = row_begin < u.rt && find_unit(p, u, blockIdx.x, true, w);
+        pdl_wait();
+        pdl_trigger();
+        if (!any) return;
+        for (int i = row_begin + warp; i < min(row_begin + JOIN_ROWS, u.rt); i += 4) {
+            const int row = w.tile * u.rt + i;
+            if (row >= w.s.nq * u.g) break;
+            const int tok = row / u.g, keys = w.s.kv - w.s.nq + tok + 1;
+            const int n = min(w.n_splits, (keys + w.chunk - 1) / w.chunk);     // units that saw a key of this row
+            T* o = reinterpret_cast<T*>(a.o) + (w.s.q0 + tok) * a.o_stride + (long long)(w.head * u.g + row % u.g) * a.hd;
+            join_row(o, a.hd, n, [&](int j) { return part_row(a, u, w.slot + j, i, a.hd); });
+        }
+        return;
+    }
+    const int c = blockIdx.x - n1 + 1;
+    ShareStart st;
+    Seq s = {0, 0, 0};
+    int tile = 0, head = 0, step = 0, c0 = 0;
+    long long begin = 0;                        // of the item, from the first step of all
+    bool any = row_begin < us.rt && find_share(p, us, c, sm, st);
+    if (any) {
+        s = load_seq(p, st.b);
+        locate_step(us, s, p.Hkv, st.off, tile, head, step);
+        begin = c * st.share - step;
+        c0 = (int)(begin / st.share);
+        any = step > 0 && c0 == c - 1;
+    }
     pdl_wait();
     pdl_trigger();
     if (!any) return;
-    const int lane = threadIdx.x & 31, rows = w.s.nq * u.g;
-    for (int i = row_begin + (threadIdx.x >> 5); i < min(row_begin + JOIN_ROWS, u.rt); i += 4) {
-        const int row = w.tile * u.rt + i;
-        if (row >= rows) break;
-        const int tok = row / u.g, keys = w.s.kv - w.s.nq + tok + 1;
-        const int n = min(w.n_splits, (keys + w.chunk - 1) / w.chunk);     // units that saw a key of this row
-        float m = NEG_BIG;
-        for (int j = lane; j < n; j += 32) m = fmaxf(m, part_row(a, u, w.slot + j, i, a.hd)[a.hd]);
-        m = warp_max(m);
-        float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < n; ++j) {
-            const float* r = part_row(a, u, w.slot + j, i, a.hd);
-            const float f = exp2f(r[a.hd] - m);
-            l += f * r[a.hd + 1];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c * 32 + lane < a.hd) acc[c] += f * r[c * 32 + lane];
-        }
-        const float inv = 1.0f / l;
-        T* o = reinterpret_cast<T*>(a.o) + (w.s.q0 + tok) * a.o_stride + (long long)(w.head * u.g + row % u.g) * a.hd;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (c * 32 + lane < a.hd) o[c * 32 + lane] = from_f<T>(acc[c] * inv);
+    for (int i = row_begin + warp; i < min(row_begin + JOIN_ROWS, us.rt); i += 4) {
+        const int row = tile * us.rt + i;
+        if (row >= s.nq * us.g) break;
+        const int tok = row / us.g, keys = s.kv - s.nq + tok + 1;
+        const long long last = begin + (keys + STEP_KEYS - 1) / STEP_KEYS - 1;  // the step of the row's last key
+        const int n = (int)(last / st.share) - c0 + 1;
+        T* o = reinterpret_cast<T*>(a.o) + (s.q0 + tok) * a.o_stride + (long long)(head * us.g + row % us.g) * a.hd;
+        // a share that begins with the item, or inside it, has it in its first slot
+        join_row(o, a.hd, n, [&](int j) {
+            return part_row(a, us, 2 * (c0 + j) + (j == 0 && begin != c0 * st.share ? 1 : 0), i, a.hd);
+        });
     }
 }
 
@@ -447,12 +484,14 @@ UnitPlan simt_plan(const PagedArgs& p, int H) {
     return make_plan(p, H, (long long)p.max_q * (H / p.Hkv) <= 2 ? 2 : 16, 1, ANY, 256, 64, 148 * 8);
 }
 
-// bf16: sequences of at most `few` rows per key head go to the warp-level kernel, those of more to
-// the tcgen05 kernel, which head widths of 64 and 128 have (and pools whose rows TMA can count).
+// bf16: sequences of at most FEW_ROWS rows per key head go to the warp-level kernel, those of more
+// to the tcgen05 kernel, which head widths of 64 and 128 have (and pools whose rows TMA can count).
 constexpr int FEW_ROWS = 16;
 struct Bf16Plans {
     bool tc;
-    UnitPlan u_mma, u_tc;
+    UnitPlan u_mma;
+    SharePlan u_tc;
+    size_t floats;              // of partial states
 };
 Bf16Plans bf16_plans(const PagedArgs& p, int H, int hd) {
     Bf16Plans b;
@@ -462,9 +501,18 @@ Bf16Plans bf16_plans(const PagedArgs& p, int H, int hd) {
     PagedArgs few = p;              // its bounds
     if (b.tc) few.max_q = FEW_ROWS / g < 1 ? 1 : FEW_ROWS / g;
     b.u_mma = make_plan(few, H, 16, 1, b.tc ? FEW_ROWS : ANY, 256, 64, 148 * 12);
+    b.floats = (size_t)b.u_mma.slots * b.u_mma.rt * (hd + 2);
+    b.u_tc = {};
     if (b.tc) {
-        b.u_tc = make_plan(p, H, 128 / g * g * 2, FEW_ROWS + 1, ANY, 512, 128, 148 * 2);
-        b.u_tc.part = (long long)b.u_mma.slots * b.u_mma.rt * (hd + 2);
+        b.u_tc.g = g;
+        b.u_tc.toks = 128 / g * paged_tc_stages(hd);
+        b.u_tc.rt = b.u_tc.toks * g;
+        b.u_tc.rows_lo = FEW_ROWS + 1;
+        b.u_tc.ctas = sm_count();
+        // items of a few steps: cutting them would cost more than an uneven end
+        b.u_tc.whole = p.max_kv <= 4 * STEP_KEYS;
+        b.u_tc.part = (long long)b.floats;
+        if (!b.u_tc.whole) b.floats += (size_t)2 * b.u_tc.ctas * b.u_tc.rt * (hd + 2);
     }
     return b;
 }
@@ -508,10 +556,7 @@ size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16) {
         const UnitPlan u = simt_plan(p, H);
         return (size_t)u.slots * u.rt * (hd + 2) * sizeof(float);
     }
-    const Bf16Plans b = bf16_plans(p, H, hd);
-    size_t n = (size_t)b.u_mma.slots * b.u_mma.rt;
-    if (b.tc) n += (size_t)b.u_tc.slots * b.u_tc.rt;
-    return n * (hd + 2) * sizeof(float);
+    return bf16_plans(p, H, hd).floats * sizeof(float);
 }
 
 template <>
@@ -520,7 +565,8 @@ cudaError_t launch_paged_attention<float>(Launch L, const PagedArgs& p, const Pa
     cudaError_t e = u.rt == 2 ? run_simt_hd<float, 1>(L, p, a, u) : run_simt_hd<float, 8>(L, p, a, u);
     const int n = join_items(u, plan_items(p, u));
     if (e != cudaSuccess || n == 0) return e;
-    return launch_k(L, k_paged_join<float>, dim3(n, (u.rt + JOIN_ROWS - 1) / JOIN_ROWS), 128, 0, p, a, u, u, n);
+    return launch_k(L, k_paged_join<float>, dim3(n, (u.rt + JOIN_ROWS - 1) / JOIN_ROWS), 128, 0, p, a, u, n,
+                    SharePlan{});
 }
 template <>
 cudaError_t launch_paged_attention<bf16>(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
@@ -536,11 +582,11 @@ cudaError_t launch_paged_attention<bf16>(Launch L, const PagedArgs& p, const Pag
     }
     if (e == cudaSuccess && b.tc) e = launch_paged_tc(L, p, a, b.u_tc);
     if (e != cudaSuccess) return e;
-    const int n1 = join_items(b.u_mma, mma_items), n2 = b.tc ? join_items(b.u_tc, plan_items(p, b.u_tc)) : 0;
+    const int n1 = join_items(b.u_mma, mma_items), n2 = b.tc && !b.u_tc.whole ? b.u_tc.ctas - 1 : 0;
     if (n1 + n2 == 0) return e;
     const int rt = n2 ? b.u_tc.rt : b.u_mma.rt;
-    return launch_k(L, k_paged_join<bf16>, dim3(n1 + n2, (rt + JOIN_ROWS - 1) / JOIN_ROWS), 128, 0, p, a, b.u_mma,
-                    b.tc ? b.u_tc : b.u_mma, n1);
+    return launch_k(L, k_paged_join<bf16>, dim3(n1 + n2, (rt + JOIN_ROWS - 1) / JOIN_ROWS), 128, 0, p, a, b.u_mma, n1,
+                    b.u_tc);
 }
 
 }  // namespace rlt

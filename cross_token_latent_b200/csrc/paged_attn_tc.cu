@@ -1,17 +1,22 @@
 // Attention of many new rows over a paged cache on the sm_100a tensor cores (bf16, head_dim 64 or
-// 128).  A CTA takes a tile of one key head's rows, two stages of up to 128 (rows of a group of
-// query heads beside each other, so that shared keys are read once), against the keys of its unit
-// in tiles of 128:
-//   warp 8      TMA producer: the query tiles once, then K and V tiles alternately into a ring; a
-//               tile is as many boxes as it has pages, one lane each
-//   warp 9      TMEM allocation; the MMAs: S_s = Q_s K^T into the stage's 128 TMEM columns, then
-//               O_s += P_s V with P_s read from TMEM and V as it lies in the page (MN-major)
-//   warps 0-3   softmax of stage 0, warps 4-7 of stage 1, a thread per row: the scores leave TMEM
-//               once, P_s goes back as bf16 over the scores' own columns.
-// While one stage's rows are in the softmax the tensor core works on the other stage.  The
-// running maximum moves only when it grew by more than 2^8 (RESCALE): a smaller maximum is as good
-// a reference for the exponentials, and the accumulator then seldom has to be rescaled; a stage's
-// O is final when its next scores have arrived, because the MMAs complete in order.
+// 128).  One CTA per SM takes an equal share of all the work (paged.cuh) and walks through the items
+// in it.  An item is a tile of one key head's rows, two stages of up to 128 (rows of a group of query
+// heads beside each other, so that shared keys are read once), against key tiles of 128:
+//   warps 0-3    softmax of stage 0, warps 4-7 of stage 1, a thread per row: the scores leave TMEM
+//                once, P_s goes back as bf16 over the scores' own columns
+//   warp 8       TMA producer: an item's query tiles, then K and V tiles alternately into a ring; a
+//                tile is as many boxes as it has pages, one lane each
+//   warp 9       the MMAs, stage 0 and 1 in turn: O_s += P_s V with P_s read from TMEM and V as it lies
+//                in the page (MN-major), then the next S_s = Q_s K^T into the stage's 128 TMEM columns.
+//                One elected thread issues, which keeps the descriptors in uniform registers (a thread
+//                that the compiler does not know to be alone took some 95 clocks per MMA).  A warp per
+//                stage was slower: their products interleave, both softmaxes fall in step and the
+//                tensor core idles meanwhile
+// While one stage's rows are in the softmax the tensor core works on the other stage, and an item's
+// last products and its output overlap with the next one's first loads and scores.  The running
+// maximum moves only when it grew by more than 2^8 (RESCALE): a smaller maximum is as good a
+// reference for the exponentials, and the accumulator then seldom has to be rescaled; a stage's O is
+// final when its next scores have arrived, because its MMAs complete in order.
 // Every mbarrier wait is bounded.
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -21,21 +26,27 @@ namespace rlt {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int KT = 128;                 // keys per tile
+constexpr int KT = 128;                 // keys per tile of the ring
 constexpr float RESCALE = 8.0f;         // log2: probabilities stay below 256
 
 template <int HD>
 struct TcShape {
+    static constexpr int STAGES = paged_tc_stages(HD);      // of up to 128 rows
+    static constexpr int KH = 256 / STAGES;                 // keys per block of scores: the stages' blocks fill 256 columns
+    static constexpr int NB = KT / KH;                      // blocks per key tile
     static constexpr int ATOMS = HD / 64;                   // 64-element swizzle atoms of a row
     static constexpr int Q_BYTES = 128 * HD * 2;            // one stage
     static constexpr int T_BYTES = KT * HD * 2;             // a tile of K or V
     static constexpr int SLOTS = HD == 128 ? 5 : 8;
-    static constexpr int OFF_KV = 2 * Q_BYTES;
+    static constexpr int OFF_KV = STAGES * Q_BYTES;
     static constexpr int OFF_BAR = OFF_KV + SLOTS * T_BYTES;
-    static constexpr int SMEM = OFF_BAR + 256 + 1024;
-    static constexpr uint32_t O_COL = 256;                  // S stages at 0 and 128, O stages behind
+    static constexpr int SMEM = OFF_BAR + 512 + 1024;
+    static constexpr int POLY = HD == 128 ? 2 : 2;          // of 8 exponentials, those not on the special function unit
+    static constexpr uint32_t O_COL = 256;                  // O of stage s behind: STAGES * HD = 256 columns
+    static constexpr int SOFTMAX_WARPS = 4 * STAGES;
+    static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 1;
+    static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
 };
-constexpr int TC_THREADS = 320;
 
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
@@ -43,68 +54,248 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// One thread of a converged warp, known as such to the compiler: the descriptors of the MMAs that it
+// issues then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// 2^x for two x in [-125, 0] and a little above on the multiply-add units: x = n + f with n the nearest
+// whole number, 2^f by the polynomial of degree 3 with the smallest relative error on [-1/2, 1/2]
+// (equal ripple, 2^-13.7; the results are rounded to bf16), n added to the exponent.  The special
+// function unit gives 16 exponentials a clock and would hold the tensor core up.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+    x.x = fmaxf(x.x, -125.f);
+    x.y = fmaxf(x.y, -125.f);
+    const float big = 12582912.f;                   // 1.5 * 2^23: a sum's low bits are the whole part
+    const float2 t = add2(x, make_float2(big, big));
+    const float2 n = add2(t, make_float2(-big, -big));
+    const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+    float2 r = fma2(f, make_float2(0.05517166852951050f, 0.05517166852951050f),
+                    make_float2(0.24261112511157990f, 0.24261112511157990f));
+    r = fma2(r, f, make_float2(0.69326096773147583f, 0.69326096773147583f));
+    r = fma2(r, f, make_float2(0.99992805719375610f, 0.99992805719375610f));
+    r.x = __int_as_float(__float_as_int(r.x) + (__float_as_int(t.x) << 23));
+    r.y = __int_as_float(__float_as_int(r.y) + (__float_as_int(t.y) << 23));
+    return r;
+}
+
+// Probabilities of 32 scores (of scaled scores less the maximum, bf16, two to a word) into the TMEM
+// columns at t_p, and their sum.  POLY of every 8 pairs take the polynomial.
+template <int POLY>
+__device__ __forceinline__ float softmax32(const uint32_t (&x)[32], uint32_t t_p, float c2, float neg) {
+    const float2 cc = make_float2(c2, c2), nn = make_float2(neg, neg);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float2 y = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, nn);
+        if (i % 8 * POLY / 8 != (i % 8 + 1) * POLY / 8) {
+            y = ex2_poly(y);
+        } else {
+            y.x = ex2_approx(y.x);
+            y.y = ex2_approx(y.y);
+        }
+        __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
+        pk[i] = *reinterpret_cast<uint32_t*>(&h);
+        sum[i & 1] = add2(sum[i & 1], y);
+    }
+    tmem_st16_async(t_p, pk);
+    sum[0] = add2(sum[0], sum[1]);
+    return sum[0].x + sum[0].y;
+}
+__device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
+    float m[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        m[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
+#pragma unroll
+        for (int i = 8; i < 32; i += 8) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4])));
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// Columns behind `seen` of 32 scores become -inf.
+__device__ __forceinline__ void mask32(uint32_t (&x)[32], int seen) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i > seen) x[i] = 0xff800000u;
+}
+
+// One stretch of a share: steps [step, step + n) of an item.  A warp walks through its CTA's share
+// item by item; all warps do so alike.
+struct Walk {
+    int b, tile, head, step, n;
+    Seq s;
+    int tiles, steps;           // of the sequence; of the item
+    long long left;             // steps of the share, this stretch's among them
+
+    __device__ __forceinline__ void enter(const PagedArgs&, const SharePlan& u) {
+        steps = share_steps(u, s, tile);
+        n = (int)(left < steps - step ? left : steps - step);
+    }
+    __device__ __forceinline__ void begin(const PagedArgs& p, const SharePlan& u, const ShareStart& st, int index) {
+        const long long end = st.share * (index + 1);
+        left = (end < st.total ? end : st.total) - st.share * index;
+        b = st.b;
+        s = load_seq(p, b);
+        tiles = share_tiles(u, s);
+        locate_step(u, s, p.Hkv, st.off, tile, head, step);
+        enter(p, u);
+    }
+    __device__ __forceinline__ bool next(const PagedArgs& p, const SharePlan& u) {
+        left -= n;
+        if (left <= 0) return false;
+        step = 0;
+        if (++head == p.Hkv) {
+            head = 0;
+            if (++tile >= tiles) {
+                // the next sequence with work, 32 at a time
+                tile = 0;
+                const int lane = threadIdx.x & 31;
+                int b0 = b + 1;
+                unsigned hit = 0;
+                for (; b0 < p.B; b0 += 32) {
+                    Seq t = {0, 0, 0};
+                    if (b0 + lane < p.B) t = load_seq(p, b0 + lane);
+                    hit = __ballot_sync(0xffffffffu, share_tiles(u, t) > 0);
+                    if (hit) {
+                        const int src = __ffs(hit) - 1;
+                        b = b0 + src;
+                        s.q0 = __shfl_sync(0xffffffffu, t.q0, src);
+                        s.nq = __shfl_sync(0xffffffffu, t.nq, src);
+                        s.kv = __shfl_sync(0xffffffffu, t.kv, src);
+                        break;
+                    }
+                }
+                if (!hit) return false;
+                tiles = share_tiles(u, s);
+            }
+        }
+        enter(p, u);
+        return true;
+    }
+};
+// What a stretch asks of the stages.
 template <int HD>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+struct Stretch {
+    using S = TcShape<HD>;
+    int k_begin, k_end;         // keys [k_begin, k_end)
+    int rows[S::STAGES], nh[S::STAGES];     // of each stage: rows, blocks of KH keys
+    int blocks, tiles;          // the longest stage's blocks and key tiles
+
+    __device__ __forceinline__ Stretch(const Walk& w, const SharePlan& u) {
+        const int row0 = w.tile * u.rt, half = u.rt / S::STAGES, ctx = w.s.kv - w.s.nq;
+        k_begin = w.step * STEP_KEYS;
+        k_end = 0;
+        blocks = 0;
+#pragma unroll
+        for (int s = 0; s < S::STAGES; ++s) {
+            rows[s] = max(0, min(half, w.s.nq * u.g - row0 - s * half));
+            int keys = rows[s] > 0 ? ctx + (row0 + s * half + rows[s] - 1) / u.g + 1 : 0;
+            if (!u.whole) keys = min(keys, (w.step + w.n) * STEP_KEYS);
+            nh[s] = max(0, (keys - k_begin + S::KH - 1) / S::KH);
+            k_end = max(k_end, keys);
+            // the same in every lane, and known as such: loops over them keep a warp converged
+            nh[s] = __shfl_sync(0xffffffffu, nh[s], 0);
+            blocks = max(blocks, nh[s]);
+        }
+        k_end = __shfl_sync(0xffffffffu, k_end, 0);
+        tiles = (blocks + S::NB - 1) / S::NB;
+    }
+    // of a stage that is no compile-time constant
+    __device__ __forceinline__ int pick(const int (&v)[S::STAGES], int s) const {
+        int x = v[0];
+#pragma unroll
+        for (int i = 1; i < S::STAGES; ++i) x = s == i ? v[i] : x;
+        return x;
+    }
+};
+
+// A ring position: slot and the parity of its round.
+template <int SLOTS>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == SLOTS) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(TcShape<HD>::THREADS, 1)
 k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKV, PagedArgs p,
-           PagedAttnArgs a, UnitPlan u, int q_box_bytes) {
+           PagedAttnArgs a, SharePlan u, int q_box_bytes) {
     using S = TcShape<HD>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
-    uint64_t* kv_full = q_full + 1;             // [SLOTS]
+    uint64_t* q_empty = q_full + 1;             // an item's last scores are computed
+    uint64_t* kv_full = q_empty + 1;            // [SLOTS]
     uint64_t* kv_empty = kv_full + S::SLOTS;    // [SLOTS]
-    uint64_t* s_full = kv_empty + S::SLOTS;     // [2] scores of tile j (phase j)
-    uint64_t* p_full = s_full + 2;              // [2] probabilities of tile j, O rescaled
-    uint64_t* o_done = p_full + 2;              // [2] the stage's last product
-    uint64_t* drained = o_done + 2;             // after a timeout: the MMAs issued have completed
+    uint64_t* s_full = kv_empty + S::SLOTS;     // [stage] the next block's scores
+    uint64_t* p_full = s_full + S::STAGES;      // [stage] its probabilities, O rescaled
+    uint64_t* o_done = p_full + S::STAGES;      // [stage] an item's last product
+    uint64_t* tail_full = o_done + S::STAGES;          // a V tile whose end is to be cleared
+    uint64_t* drained = tail_full + 1;          // after a timeout: the MMAs issued have completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     __shared__ int abort_flag;
+    __shared__ ShareSmem share_sm;
 
     // No wait for the kernel in front here: it is the one that takes this batch's other sequences, it
     // lets this one start only behind its own wait for what came before, and neither reads what the
     // other writes.  The wait stands at the end, so that this kernel's completion covers that one's.
-    Unit w;
-    if (!find_unit(p, u, blockIdx.x, false, w)) {
+    ShareStart st;
+    if (!find_share(p, u, blockIdx.x, share_sm, st)) {
         pdl_trigger();
         pdl_wait();
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = u.rt / 2;                  // rows per stage: whole tokens
-    const int row0 = w.tile * u.rt, ctx = w.s.kv - w.s.nq;
-    const int k_begin = w.split * w.chunk;
-    int rows[2], nt[2];                         // of each stage: rows, key tiles
-    int k_end = 0;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        rows[s] = max(0, min(half, w.s.nq * u.g - row0 - s * half));
-        const int keys = rows[s] > 0 ? min(ctx + (row0 + s * half + rows[s] - 1) / u.g + 1, k_begin + w.chunk) : 0;
-        nt[s] = max(0, (keys - k_begin + KT - 1) / KT);
-        k_end = max(k_end, keys);
-    }
-    const int tiles = max(nt[0], nt[1]);
-    if (tiles == 0) {
-        pdl_trigger();
-        pdl_wait();
-        return;
-    }
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int half = u.rt / S::STAGES;          // rows per stage: whole tokens
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int s = 0; s < S::SLOTS; ++s) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 4);
-            mbar_init(&o_done[s], 1);
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_done[i], 1);
         }
+        mbar_init(tail_full, 1);
         mbar_init(drained, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) {
+    if (warp == S::ISSUER) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -116,200 +307,92 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     // behind the allocation, which a kernel that starts early could otherwise get in front of
     pdl_trigger();
 
-    if (warp == 8) {
-        // lane i loads atom i % ATOMS of page i / ATOMS of a tile
-        const int page_rows = min(KT, 1 << p.page_shift);
-        const int pg = lane / S::ATOMS, atom = lane % S::ATOMS;
-        if (lane == 0) mbar_expect_tx(q_full, (nt[0] > 0 ? q_box_bytes : 0) + (nt[1] > 0 ? q_box_bytes : 0));
-        __syncwarp();
-        if (lane < 2 * S::ATOMS && nt[pg] > 0)
-            tma_load_3d(smem + pg * S::Q_BYTES + atom * 128 * 128, &tmQ, q_full, 64 * atom, w.head * u.g,
-                        w.s.q0 + (row0 + pg * half) / u.g);
-        bool ok = true;
-        int done = 0;
-        for (int j = 0; j < tiles && ok; ++j) {
-            const int key = k_begin + j * KT + pg * page_rows;
-            const bool mine = pg * page_rows < KT && key < k_end;
-            const int boxes = min(KT / page_rows, (k_end - k_begin - j * KT + page_rows - 1) / page_rows) * S::ATOMS;
-            const int page = mine ? max(load_page(p, w.b, key), 0) : 0;
-            const int in_page = key & ((1 << p.page_shift) - 1);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const int item = 2 * j + kv, slot = item % S::SLOTS;
-                ok = mbar_wait(&kv_empty[slot], ((item / S::SLOTS) & 1) ^ 1, &abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) mbar_expect_tx(&kv_full[slot], boxes * page_rows * 128);
-                __syncwarp();
-                if (mine)
-                    tma_load_2d(smem + S::OFF_KV + slot * S::T_BYTES + atom * KT * 128 + pg * page_rows * 128, &tmKV,
-                                &kv_full[slot], 64 * atom,
-                                ((((page * 2 + kv) * p.Hkv + w.head) << p.page_shift)) + in_page);
-                done = item + 1;
-            }
-        }
-        if (!ok) {
-            abort_flag = 1;
-            // the copies in flight land before the shared memory is given back
-            if (lane == 0) {
-                mbar_wait(q_full, 0, nullptr);
-                for (int i = max(0, done - S::SLOTS); i < done; ++i)
-                    mbar_wait(&kv_full[i % S::SLOTS], (i / S::SLOTS) & 1, nullptr);
-            }
-        }
-    } else if (warp == 9) {
-        constexpr uint32_t id_s = idesc_bf16(128, KT), id_o = idesc_bf16(128, HD) | IDESC_B_MN;
-        auto wait_kv = [&](int item) -> bool {
-            const bool ok = mbar_wait(&kv_full[item % S::SLOTS], (item / S::SLOTS) & 1, &abort_flag);
-            return __all_sync(0xffffffffu, ok);
-        };
-        auto issue_s = [&](int s, int j) {      // S_s = Q_s K_j^T
-            if (lane == 0) {
-                const uint8_t* kb = smem + S::OFF_KV + ((2 * j) % S::SLOTS) * S::T_BYTES;
-#pragma unroll
-                for (int at = 0; at < S::ATOMS; ++at) {
-                    const uint64_t dq = sdesc_sw128(smem + s * S::Q_BYTES + at * 128 * 128);
-                    const uint64_t dk = sdesc_sw128(kb + at * KT * 128);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) umma(tmem + s * 128, dq + 2 * k, dk + 2 * k, id_s, (at | k) != 0);
-                }
-                umma_commit(&s_full[s]);
-            }
-            __syncwarp();
-        };
-        bool ok = mbar_wait(q_full, 0, &abort_flag);
-        ok = __all_sync(0xffffffffu, ok) && wait_kv(0);
-        if (ok) {
-            tc_fence_after();
-            for (int s = 0; s < 2; ++s)
-                if (nt[s] > 0) issue_s(s, 0);
-            if (lane == 0) umma_commit(&kv_empty[0]);
-            for (int j = 0; j < tiles; ++j) {
-                const int item = 2 * j + 1, slot = item % S::SLOTS;
-                uint8_t* vb = smem + S::OFF_KV + slot * S::T_BYTES;
-                if (!(ok = wait_kv(item))) break;
-                const int have = k_end - k_begin - j * KT;
-                if (have < KT) {
-                    // slots behind the last key hold anything, and 0 * NaN is NaN: they become zeros
-                    for (int i = lane; i < (KT - have) * S::ATOMS * 8; i += 32) {
-                        const int piece = i & 7, at = (i >> 3) % S::ATOMS, r = have + (i >> 3) / S::ATOMS;
-                        *reinterpret_cast<uint4*>(vb + at * KT * 128 + r * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (j + 1 < tiles && !(ok = wait_kv(item + 1))) break;
-                for (int s = 0; s < 2; ++s) {
-                    if (j >= nt[s]) continue;
-                    ok = mbar_wait(&p_full[s], j & 1, &abort_flag);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t dv = sdesc_mn_sw128(vb, KT * 128);
-#pragma unroll
-                        for (int k = 0; k < KT / 16; ++k)
-                            umma_ta(tmem + S::O_COL + s * HD, tmem + s * 128 + k * 8, dv + k * (16 * 128 >> 4), id_o,
-                                    (j | k) != 0);
-                        if (j + 1 == nt[s]) umma_commit(&o_done[s]);
-                    }
-                    __syncwarp();
-                    if (j + 1 < nt[s]) issue_s(s, j + 1);
-                }
-                if (!ok) break;
-                if (lane == 0) {
-                    umma_commit(&kv_empty[slot]);
-                    if (j + 1 < tiles) umma_commit(&kv_empty[(item + 1) % S::SLOTS]);
-                }
-            }
-        }
-        if (!ok) {
-            abort_flag = 1;
-            if (lane == 0) {
-                umma_commit(drained);
-                mbar_wait(drained, 0, nullptr);
-            }
-        }
-    } else {
+    Walk w;
+    w.begin(p, u, st, blockIdx.x);
+    if (warp < S::SOFTMAX_WARPS) {
         const int s = warp >> 2, r = (warp & 3) * 32 + lane;        // stage, row of the stage
-        const uint32_t t_s = tmem + s * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t t_s = tmem + s * S::KH + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_o = tmem + S::O_COL + s * HD + ((uint32_t)((warp & 3) * 32) << 16);
-        const int row = row0 + s * half + r;
-        const int limit = r < rows[s] ? ctx + row / u.g - k_begin : -1;     // last key, from the unit's first
         const float c2 = a.scale * LOG2E;
-        float m = -INFINITY, l = 0.f;           // m of the scaled scores
-        bool ok = true;
-        for (int j = 0; j < nt[s]; ++j) {
-            ok = mbar_wait(&s_full[s], j & 1, &abort_flag);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            tc_fence_after();
-            uint32_t x[4][32];
+        uint32_t s_phase = 0, o_phase = 0;
+        bool ok = true, first = true;
+        do {
+            const Stretch<HD> x_(w, u);
+            const int nh = x_.pick(x_.nh, s);
+            const bool mine = r < x_.pick(x_.rows, s), whole = w.n == w.steps;
+            const int row = w.tile * u.rt + s * half + r;
+            const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+            first = false;
+            if (nh == 0) continue;
+            const int limit = mine ? w.s.kv - w.s.nq + row / u.g - x_.k_begin : -1;    // last key, from the first
+            float m = -INFINITY, l = 0.f;       // m of the scaled scores
+            for (int h = 0; h < nh; ++h) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], s_phase, &abort_flag));
+                if (!ok) break;
+                s_phase ^= 1;
+                tc_fence_after();
+                const int seen = limit - h * S::KH;         // columns 0 .. seen of this block are seen
+                const bool masked = __any_sync(0xffffffffu, seen < S::KH - 1);
+                float mx = -INFINITY;
+                // The scores are read twice, for the maximum and for the exponentials: keeping them would take
+                // registers that there are none of at this number of warps.
+                uint32_t x[2][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_async(t_s + 32 * c, x[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_wait_ld(x[c]);
-            const int seen = limit - j * KT;    // columns 0 .. seen of this tile are seen
-            if (__any_sync(0xffffffffu, seen < KT - 1)) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * c + i > seen) x[c][i] = 0xff800000u;       // -inf
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[c][i]));
-            mx *= c2;
-            // (a first maximum needs no rescale: the first product overwrites O, and l is 0)
-            const bool grow = mx > m + RESCALE || m == -INFINITY;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float to = grow ? mx : m;
-                const float al = m == -INFINITY ? 1.f : ex2_approx(m - to);
-                l *= al;
-                m = to;
-                if (j > 0) {
+                for (int c = 0; c < S::KH / 32; c += 2) {
+                    tmem_ld32_async(t_s + 32 * c, x[0]);
+                    tmem_ld32_async(t_s + 32 * c + 32, x[1]);
+                    tmem_wait_ld(x[0]);
+                    tmem_wait_ld(x[1]);
+                    if (masked) {
+                        mask32(x[0], seen - 32 * c);
+                        mask32(x[1], seen - 32 * c - 32);
+                    }
+                    mx = fmaxf(mx, fmaxf(max32(x[0]), max32(x[1])));
+                }
+                mx *= c2;
+                // (a first maximum needs no rescale: the first product overwrites O, and l is 0)
+                const bool grow = mx > m + RESCALE || m == -INFINITY;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? mx : m;
+                    const float al = m == -INFINITY ? 1.f : ex2_approx(m - to);
+                    l *= al;
+                    m = to;
+                    if (h > 0) {
 #pragma unroll 1
-                    for (int c = 0; c < HD; c += 32) {
-                        float ov[32];
-                        tmem_ld32(t_o + c, ov);
+                        for (int c = 0; c < HD; c += 32) {
+                            float ov[32];
+                            tmem_ld32(t_o + c, ov);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) ov[i] *= al;
-                        tmem_st32(t_o + c, ov);
+                            for (int i = 0; i < 32; ++i) ov[i] *= al;
+                            tmem_st32(t_o + c, ov);
+                        }
                     }
                 }
-            }
-            const float neg = m == -INFINITY ? 0.f : -m;            // a row that has seen nothing yet
+                const float neg = m == -INFINITY ? 0.f : -m;        // a row that has seen nothing yet
+                // where columns are masked every exponential is exact at -inf
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float e0 = ex2_approx(fmaf(__uint_as_float(x[c][2 * i]), c2, neg));
-                    const float e1 = ex2_approx(fmaf(__uint_as_float(x[c][2 * i + 1]), c2, neg));
-                    __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
-                    pk[i] = *reinterpret_cast<uint32_t*>(&h);
-                    l += e0 + e1;
+                for (int c = 0; c < S::KH / 32; ++c) {
+                    tmem_ld32_async(t_s + 32 * c, x[0]);
+                    tmem_wait_ld(x[0]);
+                    if (masked) {
+                        mask32(x[0], seen - 32 * c);
+                        l += softmax32<0>(x[0], t_s + 16 * c, c2, neg);
+                    } else {
+                        l += softmax32<S::POLY>(x[0], t_s + 16 * c, c2, neg);
+                    }
                 }
-                tmem_st16_async(t_s + 16 * c, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[s]);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[s]);
-        }
-        if (ok && nt[s] > 0) {
-            ok = mbar_wait(&o_done[s], 0, &abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-        }
-        if (!ok) {
-            abort_flag = 1;
-            if (lane == 0) raise_flag(p.hdr, ERR_TIMEOUT);
-        } else if (nt[s] > 0) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[s], o_phase, &abort_flag));
+            if (!ok) break;
+            o_phase ^= 1;
+            // (the next item's first product waits for probabilities that come behind these reads)
             tc_fence_after();
-            const bool mine = r < rows[s];
-            if (w.n_splits > 1) {
-                float* pr = part_row(a, u, w.slot, s * half + r, HD);
+            if (!whole) {
+                float* pr = part_row(a, u, slot, s * half + r, HD);
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 32) {
                     float ov[32];
@@ -337,23 +420,186 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     }
                 }
             }
+        } while (w.next(p, u));
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) raise_flag(p.hdr, ERR_TIMEOUT);
+        }
+    } else {
+        if (warp == S::PRODUCER) {
+            // lane i loads atom i % ATOMS of page i / ATOMS of a tile
+            const int page_rows = min(KT, 1 << p.page_shift);
+            const int pg = lane / S::ATOMS, atom = lane % S::ATOMS;
+            Ring<S::SLOTS> ring;
+            uint32_t q_phase = 0, tail_phase = 0, items = 0;
+            bool ok = true;
+            do {
+                const Stretch<HD> x_(w, u);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_empty, q_phase ^ 1, &abort_flag)))) break;
+                int boxes_q = 0;
+#pragma unroll
+                for (int s = 0; s < S::STAGES; ++s) boxes_q += x_.nh[s] > 0;
+                if (lane == 0) mbar_expect_tx(q_full, boxes_q * q_box_bytes);
+                __syncwarp();
+                if (lane < S::STAGES * S::ATOMS && x_.pick(x_.nh, pg) > 0)
+                    tma_load_3d(smem + pg * S::Q_BYTES + atom * 128 * 128, &tmQ, q_full, 64 * atom, w.head * u.g,
+                                w.s.q0 + w.tile * u.toks + pg * (u.toks / S::STAGES));
+                q_phase ^= 1;
+                for (int j = 0; j < x_.tiles && ok; ++j) {
+                    const int have = x_.k_end - x_.k_begin - j * KT;        // keys from this tile on
+                    const int key = x_.k_begin + j * KT + pg * page_rows;
+                    const bool mine = pg * page_rows < min(KT, have);
+                    const int boxes = min(KT / page_rows, (have + page_rows - 1) / page_rows) * S::ATOMS;
+                    const int page = mine ? max(load_page(p, w.b, key), 0) : 0;
+                    const int in_page = key & ((1 << p.page_shift) - 1);
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[ring.slot], ring.phase ^ 1, &abort_flag));
+                        if (!ok) break;
+                        uint8_t* tile = smem + S::OFF_KV + ring.slot * S::T_BYTES;
+                        const bool tail = kv == 1 && have < KT;
+                        uint64_t* bar = tail ? tail_full : &kv_full[ring.slot];
+                        if (lane == 0) mbar_expect_tx(bar, boxes * page_rows * 128);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_2d(tile + atom * KT * 128 + pg * page_rows * 128, &tmKV, bar, 64 * atom,
+                                        (((page * 2 + kv) * p.Hkv + w.head) << p.page_shift) + in_page);
+                        if (tail) {
+                            // slots behind the last key hold anything, and 0 * NaN is NaN: they become zeros
+                            ok = __all_sync(0xffffffffu, mbar_wait(tail_full, tail_phase, &abort_flag));
+                            tail_phase ^= 1;
+                            if (!ok) break;
+                            for (int i = lane; i < (KT - have) * S::ATOMS * 8; i += 32) {
+                                const int piece = i & 7, at = (i >> 3) % S::ATOMS, r = have + (i >> 3) / S::ATOMS;
+                                *reinterpret_cast<uint4*>(tile + at * KT * 128 + r * 128 + piece * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&kv_full[ring.slot]);
+                        }
+                        ring.next();
+                        ++items;
+                    }
+                }
+                if (!ok) break;
+            } while (w.next(p, u));
+            if (!ok) {
+                abort_flag = 1;
+                // the copies in flight land before the shared memory is given back
+                if (lane == 0) {
+                    mbar_wait(q_full, q_phase ^ 1, nullptr);
+                    mbar_wait(tail_full, tail_phase ^ 1, nullptr);
+                    for (int i = 0; i < S::SLOTS && i < (int)items; ++i) {
+                        // the slot's last full round: behind the ring's position it is the round before
+                        const uint32_t ph = i < ring.slot ? ring.phase : ring.phase ^ 1;
+                        mbar_wait(&kv_full[i], ph, nullptr);
+                    }
+                }
+            }
+        } else {
+            constexpr uint32_t id_s = idesc_bf16(128, S::KH), id_o = idesc_bf16(128, HD) | IDESC_B_MN;
+            Ring<S::SLOTS> ring;
+            uint32_t q_phase = 0, p_phase[S::STAGES] = {};
+            bool ok = true;
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) umma_commit(bar);
+                __syncwarp();
+            };
+            auto wait_kv = [&](const Ring<S::SLOTS>& at) {
+                return __all_sync(0xffffffffu, mbar_wait(&kv_full[at.slot], at.phase, &abort_flag));
+            };
+            auto issue_s = [&](int s, int b, int slot) {    // S_s = Q_s K^T, block b of the K tile in `slot`
+                const uint64_t dq0 = sdesc_sw128(smem + s * S::Q_BYTES);
+                const uint64_t dk0 = sdesc_sw128(smem + S::OFF_KV + slot * S::T_BYTES + b * S::KH * 128);
+                if (elect_one()) {
+#pragma unroll
+                    for (int at = 0; at < S::ATOMS; ++at)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma(tmem + s * S::KH, dq0 + at * (128 * 128 >> 4) + 2 * k, dk0 + at * (KT * 128 >> 4) + 2 * k,
+                                 id_s, (at | k) != 0);
+                    umma_commit(&s_full[s]);
+                }
+                __syncwarp();
+            };
+            do {
+                const Stretch<HD> x_(w, u);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_full, q_phase, &abort_flag)))) break;
+                q_phase ^= 1;
+                Ring<S::SLOTS> k = ring;                    // K of tile j
+                if (!(ok = wait_kv(k))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < S::STAGES; ++s)
+                    if (x_.nh[s] > 0) issue_s(s, 0, k.slot);
+                if (S::NB == 1) commit(&kv_empty[k.slot]);
+                if (x_.blocks == 1) commit(q_empty);
+                for (int j = 0; j < x_.tiles && ok; ++j) {
+                    ring.next();
+                    const Ring<S::SLOTS> v = ring;
+                    ring.next();
+                    const bool more = j + 1 < x_.tiles;
+                    if (!(ok = wait_kv(v))) break;
+#pragma unroll
+                    for (int b = 0; b < S::NB; ++b) {
+                        const int h = j * S::NB + b;
+                        // the block behind this one is in the same K tile, or the first of the next
+                        if (b + 1 == S::NB) {
+                            k = ring;
+                            if (more && !(ok = ok && wait_kv(k))) continue;
+                        }
+                        const uint64_t dv = sdesc_mn_sw128(smem + S::OFF_KV + v.slot * S::T_BYTES + b * S::KH * 128, KT * 128);
+#pragma unroll
+                        for (int s = 0; s < S::STAGES; ++s) {
+                            if (h >= x_.nh[s] || !ok) continue;
+                            ok = __all_sync(0xffffffffu, mbar_wait(&p_full[s], p_phase[s], &abort_flag));
+                            if (!ok) continue;
+                            p_phase[s] ^= 1;
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < S::KH / 16; ++i)
+                                    umma_ta(tmem + S::O_COL + s * HD, tmem + s * S::KH + i * 8, dv + i * (16 * 128 >> 4), id_o,
+                                            (h | i) != 0);
+                                if (h + 1 == x_.nh[s]) umma_commit(&o_done[s]);
+                            }
+                            __syncwarp();
+                            if (h + 1 < x_.nh[s]) issue_s(s, (b + 1) % S::NB, k.slot);
+                        }
+                        // the K tile's last block of scores is issued
+                        if (ok && (S::NB == 1 ? more : b + 2 == S::NB)) commit(&kv_empty[k.slot]);
+                        if (ok && h + 2 == x_.blocks) commit(q_empty);
+                    }
+                    if (ok) commit(&kv_empty[v.slot]);
+                }
+                if (!ok) break;
+            } while (w.next(p, u));
+            if (!ok) {
+                abort_flag = 1;
+                if (elect_one()) {
+                    umma_commit(drained);
+                    mbar_wait(drained, 0, nullptr);
+                }
+                __syncwarp();
+            }
         }
     }
     pdl_wait();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == S::ISSUER) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
     }
 }
 
 template <int HD>
-cudaError_t run(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
+cudaError_t run(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const SharePlan& u) {
     using S = TcShape<HD>;
     cudaError_t e = cudaFuncSetAttribute(k_paged_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
-    const int toks = u.rt / 2 / u.g;            // tokens per stage
+    const int toks = u.toks / S::STAGES;        // tokens per stage
     CUtensorMap tq, tkv;
     const uint64_t qdims[3] = {(uint64_t)HD, (uint64_t)a.H, (uint64_t)p.N};
     const uint64_t qstr[2] = {(uint64_t)HD * 2, (uint64_t)a.q_stride * 2};
@@ -364,13 +610,12 @@ cudaError_t run(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const Unit
     const uint32_t kvbox[2] = {64, page < KT ? page : KT};
     if (!tma_map_bf16_new(&tq, a.q, 3, qdims, qstr, qbox) || !tma_map_bf16_new(&tkv, a.pool, 2, kvdims, kvstr, kvbox))
         return cudaErrorInvalidValue;
-    const long long grid = plan_items(p, u) + (u.slots ? u.target : 0);
-    return launch_k(L, k_paged_tc<HD>, (unsigned)grid, TC_THREADS, S::SMEM, tq, tkv, p, a, u, u.g * toks * 128 * S::ATOMS);
+    return launch_k(L, k_paged_tc<HD>, (unsigned)u.ctas, S::THREADS, S::SMEM, tq, tkv, p, a, u, u.g * toks * 128 * S::ATOMS);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_tc(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
+cudaError_t launch_paged_tc(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const SharePlan& u) {
     return a.hd == 64 ? run<64>(L, p, a, u) : run<128>(L, p, a, u);
 }
 

@@ -69,8 +69,8 @@ def attention_ref(pool, r: Ragged, q, scale=None):
     """(out, tolerance) in 64 bits for every row of a sequence, [rows, H, hd].
 
     The tolerance is a bound on what the arithmetic allows: with the score error ds (products of
-    float32 sums), every probability is off by a relative ds + 2^-21 (exponential), on the tensor
-    cores by a rounding to bf16 more; numerator and denominator both carry it, weighted by
+    float32 sums), every probability is off by a relative ds + 2^-21 (exponential; 2^-13 for the
+    polynomial of the bf16 kernels), on the tensor cores by a rounding to bf16 more; numerator and denominator both carry it, weighted by
     A = sum p |v|; sums of n terms add n 2^-24; the result is rounded once."""
     H, hd = q.shape[1], q.shape[2]
     Hkv = pool.shape[2]
@@ -92,7 +92,7 @@ def attention_ref(pool, r: Ragged, q, scale=None):
         o = torch.einsum("hgqk,hkd->hgqd", p, v)
         A = torch.einsum("hgqk,hkd->hgqd", p, v.abs())
         ds = mag.masked_fill(ahead, 0).amax(-1, keepdim=True) * (hd + 4) * 2.0 ** -24
-        rel = 2 * (ds + 2.0 ** -21 + r.kv[b] * 2.0 ** -24) + (2 * 2.0 ** -8 if dtype == "bf16" else 0)
+        rel = 2 * (ds + 2.0 ** (-13 if dtype == "bf16" else -21) + r.kv[b] * 2.0 ** -24) + (2 * 2.0 ** -8 if dtype == "bf16" else 0)
         tol = half * o.abs() + rel * A * 1.01 + 1e-30
         outs.append(o.flatten(0, 1).permute(1, 0, 2))
         tols.append(tol.flatten(0, 1).permute(1, 0, 2))
