@@ -176,6 +176,13 @@ struct SharePlan {
     int ctas;
     int whole;
     long long part;             // partial states, in floats: slots 2c and 2c + 1 are CTA c's
+    long long cuts;             // a ShareCut per CTA behind them, in floats
+};
+// Where a share begins: the item, and how many of its steps belong to the shares in front.
+struct ShareCut {
+    Seq s;
+    int tile, head, step;
+    long long begin, share;     // the item's first step among all, steps per share
 };
 
 __device__ __forceinline__ int share_tiles(const SharePlan& u, const Seq& s) {
@@ -346,17 +353,21 @@ struct PagedAttnArgs {
 };
 // A row of a cut item's partial state: head_dim accumulators (not divided by the sum), the maximum
 // (of base-2 scaled scores) and the sum.
-template <typename Plan>
-__device__ __forceinline__ float* part_row(const PagedAttnArgs& a, const Plan& u, int slot, int row, int hd) {
+__device__ __forceinline__ float* part_row(const PagedAttnArgs& a, const UnitPlan& u, int slot, int row, int hd) {
     return a.part + u.part + ((long long)slot * u.rt + row) * (hd + 2);
+}
+// The partial state of a share plan's slot, [head_dim + 2][rt]: a thread has a row of it, and rows side
+// by side make its accesses whole ones.
+__device__ __forceinline__ float* share_part(const PagedAttnArgs& a, const SharePlan& u, int slot, int hd) {
+    return a.part + u.part + (long long)slot * u.rt * (hd + 2);
 }
 size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16);
 template <typename T>
 cudaError_t launch_paged_attention(Launch L, const PagedArgs& p, const PagedAttnArgs& a);
 
 // ------------------------------------------------------------------ paged_attn_tc.cu
-// Row stages of a tile: what the accumulators of 256 TMEM columns allow.
-constexpr int paged_tc_stages(int hd) { return 256 / hd; }
+constexpr int PAGED_TC_STAGES = 2;                                  // row stages of a tile
+constexpr int paged_tc_ctas(int hd) { return hd == 64 ? 2 : 1; }    // CTAs per SM
 cudaError_t launch_paged_tc(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const SharePlan& u);
 
 // ------------------------------------------------------------------ logits.cu

@@ -13,82 +13,113 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NEG_BIG = -1e30f;
 
-// One output row of a cut item from n partial states; state j's row is at r(j).
-template <typename T, typename F>
-__device__ __forceinline__ void join_row(T* o, int hd, int n, F r) {
+// Rows i0, i0 + stride, .. (JOIN_WARP_ROWS of them, those below `rows`) of a cut item, by a warp: row i
+// is joined from n(i) partial states, state j of it at r(j, i), into o(i).  The rows' loads are in flight
+// together.
+constexpr int JOIN_WARP_ROWS = 4;
+template <typename T, typename N, typename R, typename O>
+__device__ __forceinline__ void join_rows(int i0, int stride, int rows, int hd, N n, R r, O o) {
     const int lane = threadIdx.x & 31;
-    float m = NEG_BIG;
-    for (int j = lane; j < n; j += 32) m = fmaxf(m, r(j)[hd]);
-    m = warp_max(m);
-    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < n; ++j) {
-        const float* x = r(j);
-        const float f = exp2f(x[hd] - m);
-        l += f * x[hd + 1];
+    constexpr int K = JOIN_WARP_ROWS;
+    float m[K], l[K], acc[K][4];
+    int cnt[K], most = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = i0 + k * stride;
+        cnt[k] = i < rows ? n(i) : 0;
+        most = max(most, cnt[k]);
+        m[k] = NEG_BIG;
+        l[k] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[k][c] = 0.f;
+    }
+    for (int j = 0; j < most; ++j) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (j >= cnt[k]) continue;
+            const float* x = r(j, i0 + k * stride);
+            const float2 ml = *reinterpret_cast<const float2*>(x + hd);
+            const float to = fmaxf(m[k], ml.x), f0 = exp2f(m[k] - to), f1 = exp2f(ml.x - to);
+            m[k] = to;
+            l[k] = l[k] * f0 + ml.y * f1;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c * 32 + lane < hd) acc[k][c] = acc[k][c] * f0 + x[c * 32 + lane] * f1;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (cnt[k] == 0) continue;
+        T* out = o(i0 + k * stride);
+        const float inv = 1.0f / l[k];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            if (c * 32 + lane < hd) acc[c] += f * x[c * 32 + lane];
+            if (c * 32 + lane < hd) out[c * 32 + lane] = from_f<T>(acc[k][c] * inv);
     }
-    const float inv = 1.0f / l;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        if (c * 32 + lane < hd) o[c * 32 + lane] = from_f<T>(acc[c] * inv);
 }
 
-// Joins the partial states of the cut items: a block takes 16 rows of one item, its warps row by
-// row.  The first n1 blocks of x are cut items of the plan u; with the plan us, block n1 + c - 1
-// is the item that share c begins inside of, if share c is the first to.
-constexpr int JOIN_ROWS = 16;
+// Joins the partial states of the cut items.  The first n1 blocks of x are cut items of the plan u (16
+// rows and fewer).  With the plan us, block n1 + c - 1 is the item that share c begins inside of, if
+// share c is the first to: 128 rows, a thread each, of 32 columns (y: column and row blocks).
+constexpr int JOIN_COLS = 32;
 template <typename T>
 __global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u, int n1, SharePlan us) {
-    // The kernel in front waited for its predecessor before it let this one start, so the batch's
-    // lengths may be read here; the partial states only behind the wait.
-    __shared__ ShareSmem sm;
-    const int row_begin = blockIdx.y * JOIN_ROWS, warp = threadIdx.x >> 5;
     if ((int)blockIdx.x < n1) {
+        // The kernel in front waited for its predecessor before it let this one start, so the batch's
+        // lengths may be read here; the partial states only behind the wait.
         Unit w;
-        const bool any = row_begin < u.rt && find_unit(p, u, blockIdx.x, true, w);
+        const bool any = blockIdx.y == 0 && find_unit(p, u, blockIdx.x, true, w);
         pdl_wait();
         pdl_trigger();
         if (!any) return;
-        for (int i = row_begin + warp; i < min(row_begin + JOIN_ROWS, u.rt); i += 4) {
-            const int row = w.tile * u.rt + i;
-            if (row >= w.s.nq * u.g) break;
-            const int tok = row / u.g, keys = w.s.kv - w.s.nq + tok + 1;
-            const int n = min(w.n_splits, (keys + w.chunk - 1) / w.chunk);     // units that saw a key of this row
-            T* o = reinterpret_cast<T*>(a.o) + (w.s.q0 + tok) * a.o_stride + (long long)(w.head * u.g + row % u.g) * a.hd;
-            join_row(o, a.hd, n, [&](int j) { return part_row(a, u, w.slot + j, i, a.hd); });
-        }
+        const int row0 = w.tile * u.rt, ctx = w.s.kv - w.s.nq;
+        join_rows<T>(
+            threadIdx.x >> 5, 4, min(u.rt, w.s.nq * u.g - row0), a.hd,
+            [&](int i) {                        // units that saw a key of this row
+                return min(w.n_splits, (ctx + (row0 + i) / u.g + 1 + w.chunk - 1) / w.chunk);
+            },
+            [&](int j, int i) { return part_row(a, u, w.slot + j, i, a.hd); },
+            [&](int i) {
+                return reinterpret_cast<T*>(a.o) + (w.s.q0 + (row0 + i) / u.g) * a.o_stride +
+                       (long long)(w.head * u.g + (row0 + i) % u.g) * a.hd;
+            });
         return;
-    }
-    const int c = blockIdx.x - n1 + 1;
-    ShareStart st;
-    Seq s = {0, 0, 0};
-    int tile = 0, head = 0, step = 0, c0 = 0;
-    long long begin = 0;                        // of the item, from the first step of all
-    bool any = row_begin < us.rt && find_share(p, us, c, sm, st);
-    if (any) {
-        s = load_seq(p, st.b);
-        locate_step(us, s, p.Hkv, st.off, tile, head, step);
-        begin = c * st.share - step;
-        c0 = (int)(begin / st.share);
-        any = step > 0 && c0 == c - 1;
     }
     pdl_wait();
     pdl_trigger();
-    if (!any) return;
-    for (int i = row_begin + warp; i < min(row_begin + JOIN_ROWS, us.rt); i += 4) {
-        const int row = tile * us.rt + i;
-        if (row >= s.nq * us.g) break;
-        const int tok = row / us.g, keys = s.kv - s.nq + tok + 1;
-        const long long last = begin + (keys + STEP_KEYS - 1) / STEP_KEYS - 1;  // the step of the row's last key
-        const int n = (int)(last / st.share) - c0 + 1;
-        T* o = reinterpret_cast<T*>(a.o) + (s.q0 + tok) * a.o_stride + (long long)(head * us.g + row % us.g) * a.hd;
-        // a share that begins with the item, or inside it, has it in its first slot
-        join_row(o, a.hd, n, [&](int j) {
-            return part_row(a, us, 2 * (c0 + j) + (j == 0 && begin != c0 * st.share ? 1 : 0), i, a.hd);
-        });
+    const int c = blockIdx.x - n1 + 1;
+    const ShareCut cut = reinterpret_cast<const ShareCut*>(a.part + us.cuts)[c];
+    if (cut.step == 0) return;
+    const int c0 = (int)(cut.begin / cut.share), row0 = cut.tile * us.rt;
+    const int cols = a.hd / JOIN_COLS, i = blockIdx.y / cols * 128 + threadIdx.x, col = blockIdx.y % cols * JOIN_COLS;
+    if (c0 != c - 1 || i >= us.rt || row0 + i >= cut.s.nq * us.g) return;
+    const int tok = (row0 + i) / us.g;
+    // shares up to the step of the row's last key
+    const int n = (int)((cut.begin + (cut.s.kv - cut.s.nq + tok) / STEP_KEYS) / cut.share) - c0 + 1;
+    // a share that begins with the item, or inside it, has it in its first slot
+    const int first = 2 * c0 + (cut.begin != c0 * cut.share ? 1 : 0);
+    float m = NEG_BIG, l = 0.f, acc[JOIN_COLS];
+#pragma unroll
+    for (int k = 0; k < JOIN_COLS; ++k) acc[k] = 0.f;
+    for (int j = 0; j < n; ++j) {
+        const float* x = share_part(a, us, j == 0 ? first : 2 * (c0 + j), a.hd) + i;
+        float v[JOIN_COLS];
+#pragma unroll
+        for (int k = 0; k < JOIN_COLS; ++k) v[k] = x[(col + k) * us.rt];
+        const float mj = x[a.hd * us.rt], lj = x[(a.hd + 1) * us.rt];
+        const float to = fmaxf(m, mj), f0 = exp2f(m - to), f1 = exp2f(mj - to);
+        m = to;
+        l = l * f0 + lj * f1;
+#pragma unroll
+        for (int k = 0; k < JOIN_COLS; ++k) acc[k] = acc[k] * f0 + v[k] * f1;
     }
+    const float inv = 1.0f / l;
+    T* o = reinterpret_cast<T*>(a.o) + (cut.s.q0 + tok) * a.o_stride +
+           (long long)(cut.head * us.g + (row0 + i) % us.g) * a.hd + col;
+#pragma unroll
+    for (int k = 0; k < JOIN_COLS; ++k) acc[k] *= inv;
+#pragma unroll
+    for (int k = 0; k < JOIN_COLS; k += Vec16<T>::N) st16(o + k, Vec16<T>::pack(acc + k));
 }
 
 // ------------------------------------------------------------------ CUDA cores
@@ -276,21 +307,23 @@ struct MmaShape {
     static constexpr int NT = HD / 8;                       // output tiles of 8 columns
     static constexpr int LD = HD + 4;
     static constexpr int SMEM = MMA_WARPS * 16 * LD * 4;
+    static constexpr int CTAS = HD == 128 ? 2 : (HD == 64 ? 4 : 5);      // resident per SM
 };
 
 template <int HD>
-__global__ void __launch_bounds__(MMA_WARPS * 32) k_paged_mma(PagedArgs p, PagedAttnArgs a, UnitPlan u) {
+__global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mma(PagedArgs p, PagedAttnArgs a, UnitPlan u, int units) {
     using S = MmaShape<HD>;
     extern __shared__ __align__(16) float sm[];             // [warps][16][LD]: accumulators, maximum, sum
     pdl_wait();
     pdl_trigger();
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     Unit w;
-    if (!find_unit(p, u, blockIdx.x, false, w)) return;
+    if (!find_unit(p, u, unit, false, w)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int row0 = w.tile * 16, rows = min(16, w.s.nq * u.g - row0), ctx = w.s.kv - w.s.nq;
     const int last = ctx + (row0 + rows - 1) / u.g;
     const int k_begin = w.split * w.chunk, k_end = min(last + 1, k_begin + w.chunk);
-    if (k_begin >= k_end) return;
+    if (k_begin >= k_end) continue;
     const float c2 = a.scale * LOG2E;
 
     uint32_t q[2][S::QP][S::QW];
@@ -463,6 +496,8 @@ __global__ void __launch_bounds__(MMA_WARPS * 32) k_paged_mma(PagedArgs p, Paged
                                          (long long)(w.head * u.g + row % u.g) * HD + col] = from_f<bf16>(acc / lt);
         }
     }
+    __syncthreads();
+    }
 }
 
 UnitPlan make_plan(const PagedArgs& p, int H, int rt, int rows_lo, int rows_hi, int min_chunk, int align, int target) {
@@ -505,22 +540,31 @@ Bf16Plans bf16_plans(const PagedArgs& p, int H, int hd) {
     b.u_tc = {};
     if (b.tc) {
         b.u_tc.g = g;
-        b.u_tc.toks = 128 / g * paged_tc_stages(hd);
+        b.u_tc.toks = 128 / g * PAGED_TC_STAGES;
         b.u_tc.rt = b.u_tc.toks * g;
         b.u_tc.rows_lo = FEW_ROWS + 1;
-        b.u_tc.ctas = sm_count();
+        b.u_tc.ctas = sm_count() * paged_tc_ctas(hd);
         // items of a few steps: cutting them would cost more than an uneven end
         b.u_tc.whole = p.max_kv <= 4 * STEP_KEYS;
         b.u_tc.part = (long long)b.floats;
-        if (!b.u_tc.whole) b.floats += (size_t)2 * b.u_tc.ctas * b.u_tc.rt * (hd + 2);
+        if (!b.u_tc.whole) {
+            b.floats += (size_t)2 * b.u_tc.ctas * b.u_tc.rt * (hd + 2);
+            b.floats = (b.floats + 3) / 4 * 4;
+            b.u_tc.cuts = (long long)b.floats;
+            b.floats += (size_t)b.u_tc.ctas * sizeof(ShareCut) / sizeof(float);
+        }
     }
     return b;
 }
 
 template <int HD>
-cudaError_t run_mma(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u, long long items) {
-    const long long grid = items + (u.slots ? u.target : 0);
-    return launch_k(L, k_paged_mma<HD>, (unsigned)grid, MMA_WARPS * 32, MmaShape<HD>::SMEM, p, a, u);
+cudaError_t run_mma(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u, long long items, bool beside_tc) {
+    // A block per unit (592 blocks that walk through the units took 249 us for 64 decode contexts where
+    // this takes 220), but where another kernel has the long sequences there may be few units or none,
+    // and then blocks that look for theirs in vain cost more: no more than are resident at once.
+    const int units = (int)(items + (u.slots ? u.target : 0));
+    const int most = sm_count() * MmaShape<HD>::CTAS, grid = beside_tc && units > most ? most : units;
+    return launch_k(L, k_paged_mma<HD>, (unsigned)grid, MMA_WARPS * 32, MmaShape<HD>::SMEM, p, a, u, units);
 }
 
 template <typename T, int HD, int R>
@@ -565,8 +609,7 @@ cudaError_t launch_paged_attention<float>(Launch L, const PagedArgs& p, const Pa
     cudaError_t e = u.rt == 2 ? run_simt_hd<float, 1>(L, p, a, u) : run_simt_hd<float, 8>(L, p, a, u);
     const int n = join_items(u, plan_items(p, u));
     if (e != cudaSuccess || n == 0) return e;
-    return launch_k(L, k_paged_join<float>, dim3(n, (u.rt + JOIN_ROWS - 1) / JOIN_ROWS), 128, 0, p, a, u, n,
-                    SharePlan{});
+    return launch_k(L, k_paged_join<float>, dim3(n), 128, 0, p, a, u, n, SharePlan{});
 }
 template <>
 cudaError_t launch_paged_attention<bf16>(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
@@ -575,18 +618,17 @@ cudaError_t launch_paged_attention<bf16>(Launch L, const PagedArgs& p, const Pag
     const long long mma_items = b.tc ? (long long)p.B * p.Hkv : plan_items(p, b.u_mma);
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.hd) {
-        case 16: e = run_mma<16>(L, p, a, b.u_mma, mma_items); break;
-        case 32: e = run_mma<32>(L, p, a, b.u_mma, mma_items); break;
-        case 64: e = run_mma<64>(L, p, a, b.u_mma, mma_items); break;
-        case 128: e = run_mma<128>(L, p, a, b.u_mma, mma_items); break;
+        case 16: e = run_mma<16>(L, p, a, b.u_mma, mma_items, b.tc); break;
+        case 32: e = run_mma<32>(L, p, a, b.u_mma, mma_items, b.tc); break;
+        case 64: e = run_mma<64>(L, p, a, b.u_mma, mma_items, b.tc); break;
+        case 128: e = run_mma<128>(L, p, a, b.u_mma, mma_items, b.tc); break;
     }
     if (e == cudaSuccess && b.tc) e = launch_paged_tc(L, p, a, b.u_tc);
     if (e != cudaSuccess) return e;
     const int n1 = join_items(b.u_mma, mma_items), n2 = b.tc && !b.u_tc.whole ? b.u_tc.ctas - 1 : 0;
     if (n1 + n2 == 0) return e;
-    const int rt = n2 ? b.u_tc.rt : b.u_mma.rt;
-    return launch_k(L, k_paged_join<bf16>, dim3(n1 + n2, (rt + JOIN_ROWS - 1) / JOIN_ROWS), 128, 0, p, a, b.u_mma, n1,
-                    b.u_tc);
+    const int y = n2 ? (b.u_tc.rt + 127) / 128 * (a.hd / JOIN_COLS) : 1;
+    return launch_k(L, k_paged_join<bf16>, dim3(n1 + n2, y), 128, 0, p, a, b.u_mma, n1, b.u_tc);
 }
 
 }  // namespace rlt

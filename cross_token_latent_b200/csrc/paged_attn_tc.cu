@@ -31,18 +31,20 @@ constexpr float RESCALE = 8.0f;         // log2: probabilities stay below 256
 
 template <int HD>
 struct TcShape {
-    static constexpr int STAGES = paged_tc_stages(HD);      // of up to 128 rows
-    static constexpr int KH = 256 / STAGES;                 // keys per block of scores: the stages' blocks fill 256 columns
+    static constexpr int STAGES = PAGED_TC_STAGES;          // of up to 128 rows
+    static constexpr int CTAS = paged_tc_ctas(HD);          // per SM
+    static constexpr int KH = HD;                           // keys per block of scores
     static constexpr int NB = KT / KH;                      // blocks per key tile
     static constexpr int ATOMS = HD / 64;                   // 64-element swizzle atoms of a row
     static constexpr int Q_BYTES = 128 * HD * 2;            // one stage
     static constexpr int T_BYTES = KT * HD * 2;             // a tile of K or V
-    static constexpr int SLOTS = HD == 128 ? 5 : 8;
+    static constexpr int SLOTS = HD == 128 ? 5 : 4;
     static constexpr int OFF_KV = STAGES * Q_BYTES;
     static constexpr int OFF_BAR = OFF_KV + SLOTS * T_BYTES;
-    static constexpr int SMEM = OFF_BAR + 512 + 1024;
+    static constexpr int SMEM = OFF_BAR + 256 + 1024;
     static constexpr int POLY = HD == 128 ? 2 : 2;          // of 8 exponentials, those not on the special function unit
-    static constexpr uint32_t O_COL = 256;                  // O of stage s behind: STAGES * HD = 256 columns
+    static constexpr uint32_t O_COL = STAGES * KH;          // O behind the scores
+    static constexpr uint32_t TMEM_COLS = STAGES * (KH + HD);
     static constexpr int SOFTMAX_WARPS = 4 * STAGES;
     static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 1;
     static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
@@ -247,7 +249,7 @@ struct Ring {
 };
 
 template <int HD>
-__global__ void __launch_bounds__(TcShape<HD>::THREADS, 1)
+__global__ void __launch_bounds__(TcShape<HD>::THREADS, TcShape<HD>::CTAS)
 k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKV, PagedArgs p,
            PagedAttnArgs a, SharePlan u, int q_box_bytes) {
     using S = TcShape<HD>;
@@ -270,7 +272,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     // lets this one start only behind its own wait for what came before, and neither reads what the
     // other writes.  The wait stands at the end, so that this kernel's completion covers that one's.
     ShareStart st;
+    ShareCut* cut = reinterpret_cast<ShareCut*>(a.part + u.cuts) + blockIdx.x;
     if (!find_share(p, u, blockIdx.x, share_sm, st)) {
+        if (!u.whole && threadIdx.x == 0) cut->step = 0;
         pdl_trigger();
         pdl_wait();
         return;
@@ -297,7 +301,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     }
     if (warp == S::ISSUER) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(512));
+                     "r"(S::TMEM_COLS));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     tc_fence_before();
@@ -309,6 +313,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 
     Walk w;
     w.begin(p, u, st, blockIdx.x);
+    if (!u.whole && threadIdx.x == 0) *cut = {w.s, w.tile, w.head, w.step, blockIdx.x * st.share - w.step, st.share};
     if (warp < S::SOFTMAX_WARPS) {
         const int s = warp >> 2, r = (warp & 3) * 32 + lane;        // stage, row of the stage
         const uint32_t t_s = tmem + s * S::KH + ((uint32_t)((warp & 3) * 32) << 16);
@@ -392,18 +397,20 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             // (the next item's first product waits for probabilities that come behind these reads)
             tc_fence_after();
             if (!whole) {
-                float* pr = part_row(a, u, slot, s * half + r, HD);
+                float* pr = share_part(a, u, slot, HD) + s * half + r;
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 32) {
                     float ov[32];
                     tmem_ld32(t_o + c, ov);
                     if (mine) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            *reinterpret_cast<float2*>(pr + c + i) = make_float2(ov[i], ov[i + 1]);
+                        for (int i = 0; i < 32; ++i) pr[(c + i) * u.rt] = ov[i];
                     }
                 }
-                if (mine) *reinterpret_cast<float2*>(pr + HD) = make_float2(m, l);
+                if (mine) {
+                    pr[HD * u.rt] = m;
+                    pr[(HD + 1) * u.rt] = l;
+                }
             } else {
                 const float inv = 1.0f / l;
                 bf16* o = reinterpret_cast<bf16*>(a.o) + (long long)(w.s.q0 + row / u.g) * a.o_stride +
@@ -590,7 +597,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     __syncthreads();
     if (warp == S::ISSUER) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TMEM_COLS));
     }
 }
 
