@@ -223,18 +223,19 @@ class RLTState:
             pass
 
 
-def _need(t: torch.Tensor, what: str, dtype, device, shape) -> None:
-    """ValueError unless t is a tensor of this type, device and shape (None: any size)."""
-    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what}: need {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+def _need(t: torch.Tensor, what: str, dtype, device: int, shape: tuple) -> None:
+    """ValueError unless t is a tensor of this type and shape on CUDA device number `device`."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        raise ValueError(f"{what}: need {dtype} {list(shape)} on cuda:{device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _row_stride(t: torch.Tensor, what: str) -> int:
     """Elements between the rows of [N, heads, head_dim], whose rows are contiguous."""
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    s0, s1, s2 = t.stride()
+    n, h, d = t.shape
+    if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return s0 if n > 1 else h * d
 
 
 class PagedBatch:
@@ -245,9 +246,9 @@ class PagedBatch:
     def __init__(self, model: "RLTModel", table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, N: int,
                  max_q: int, max_kv: int, page_size: int, n_kv_heads: int):
         B = kv_len.shape[0]
-        _need(table, "table", torch.int32, model.device, (B, None))
-        _need(q_start, "q_start", torch.int32, model.device, (B + 1,))
-        _need(kv_len, "kv_len", torch.int32, model.device, (B,))
+        _need(table, "table", torch.int32, model._dev, (B, table.shape[-1]))
+        _need(q_start, "q_start", torch.int32, model._dev, (B + 1,))
+        _need(kv_len, "kv_len", torch.int32, model._dev, (B,))
         if not (q_start.is_contiguous() and kv_len.is_contiguous()) or table.stride(1) != 1 or \
                 table.stride(0) < table.shape[1]:
             raise ValueError("q_start, kv_len and the rows of the page table must be contiguous")
@@ -262,10 +263,24 @@ class PagedBatch:
                                 table.data_ptr(), table.stride(0) if B > 1 else cols, int(page_size), 0,
                                 int(n_kv_heads))
         self.ref = ctypes.byref(self.c)
+        self._page = (2, self.n_kv_heads, self.page_size, model.cfg.head_dim)
+        self._ws: dict = {}                        # workspace bytes by (n_pages, n_heads)
 
-    def args(self, n_pages: int):
-        self.c.n_pages = n_pages
+    def args(self, pool: torch.Tensor):
+        """The C structure for calls on this pool [n_pages, 2, n_kv_heads, page_size, head_dim]."""
+        n = pool.shape[0]
+        _need(pool, "pool", self.model.sdtype, self.model._dev, (n, *self._page))
+        if not pool.is_contiguous():
+            raise ValueError("pool: must be contiguous")
+        self.c.n_pages = n
         return self.ref
+
+    def attention_workspace_bytes(self, n_heads: int) -> int:
+        key = (self.c.n_pages, n_heads)
+        nb = self._ws.get(key)
+        if nb is None:
+            nb = self._ws[key] = lib().rlt_paged_attention_workspace_bytes(self.model.handle, self.ref, n_heads)
+        return nb
 
 
 class RLTModel:
@@ -278,6 +293,7 @@ class RLTModel:
         self.device = torch.device(device)
         if self.device.index is None:
             self.device = torch.device(self.device.type, torch.cuda.current_device())
+        self._dev = self.device.index
         self.max_pos = int(max_pos)
         self.sdtype = torch.bfloat16 if cfg.dtype == "bf16" else torch.float32
         self._c = make_config(cfg, max_pos)
@@ -326,6 +342,10 @@ class RLTModel:
     @property
     def launch_count(self) -> int:
         return lib().rlt_launch_count(self.handle)
+
+    def _raw_stream(self) -> int:
+        """The current stream of the model's device, as the C ABI takes it."""
+        return torch._C._cuda_getCurrentRawStream(self._dev)
 
     def _workspace(self, key, nbytes: int) -> torch.Tensor:
         buf = self._ws.get(key)
@@ -429,40 +449,41 @@ class RLTModel:
         return PagedBatch(self, table, q_start, kv_len, N, max_q, max_kv, page_size,
                           self.cfg.n_heads if n_kv_heads is None else n_kv_heads)
 
-    def _pool(self, batch: PagedBatch, pool: torch.Tensor):
+    def _paged(self, batch: PagedBatch, pool: torch.Tensor):
         if batch.model is not self:
             raise ValueError("the batch was made for another model")
-        _need(pool, "pool", self.sdtype, self.device, (None, 2, batch.n_kv_heads, batch.page_size, self.cfg.head_dim))
-        if not pool.is_contiguous():
-            raise ValueError("pool: must be contiguous")
-        return batch.args(pool.shape[0])
+        return batch.args(pool)
 
     def paged_append(self, batch: PagedBatch, pool: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                      q: torch.Tensor | None = None, q_out: torch.Tensor | None = None) -> torch.Tensor | None:
         """rlt_paged_append: k, v [N, n_kv_heads, head_dim] (float32 or the model's dtype) into the pool
         [n_pages, 2, n_kv_heads, page_size, head_dim], the keys rotated; with q [N, n_heads, head_dim] the
         rotated queries are returned (in q_out)."""
-        ref = self._pool(batch, pool)
-        N, hd = batch.N, self.cfg.head_dim
-        if k.dtype != torch.float32 and k.dtype != self.sdtype:
-            raise ValueError(f"k: need float32 or {self.sdtype}, got {k.dtype}")
-        _need(k, "k", k.dtype, self.device, (N, batch.n_kv_heads, hd))
-        _need(v, "v", k.dtype, self.device, (N, batch.n_kv_heads, hd))
-        H = qs = os = 0
+        ref = self._paged(batch, pool)
+        N, hd, dev, dt = batch.N, self.cfg.head_dim, self._dev, k.dtype
+        if dt is not torch.float32 and dt is not self.sdtype:
+            raise ValueError(f"k: need float32 or {self.sdtype}, got {dt}")
+        shape = (N, batch.n_kv_heads, hd)
+        _need(k, "k", dt, dev, shape)
+        _need(v, "v", dt, dev, shape)
+        H = qs = os = qp = op = 0
         if q is None:
             if q_out is not None:
                 raise ValueError("q_out without q")
         else:
             H = q.shape[1]
-            _need(q, "q", k.dtype, self.device, (N, None, hd))
+            shape = (N, H, hd)
+            _need(q, "q", dt, dev, shape)
             if q_out is None:
-                q_out = torch.empty((N, H, hd), dtype=self.sdtype, device=self.device)
-            _need(q_out, "q_out", self.sdtype, self.device, (N, H, hd))
-            qs, os = _row_stride(q, "q"), _row_stride(q_out, "q_out")
-        _check(lib().rlt_paged_append(self.handle, ref, pool.data_ptr(), k.data_ptr(), _row_stride(k, "k"),
-                                      v.data_ptr(), _row_stride(v, "v"), _ptr(q), qs, H, _ptr(q_out), os,
-                                      RLT_F32 if k.dtype == torch.float32 else RLT_BF16, _stream()),
-               "rlt_paged_append")
+                q_out = torch.empty(shape, dtype=self.sdtype, device=self.device)
+            else:
+                _need(q_out, "q_out", self.sdtype, dev, shape)
+            qs, os, qp, op = _row_stride(q, "q"), _row_stride(q_out, "q_out"), q.data_ptr(), q_out.data_ptr()
+        code = lib().rlt_paged_append(self.handle, ref, pool.data_ptr(), k.data_ptr(), _row_stride(k, "k"),
+                                      v.data_ptr(), _row_stride(v, "v"), qp, qs, H, op, os,
+                                      RLT_F32 if dt is torch.float32 else RLT_BF16, self._raw_stream())
+        if code:
+            raise RLTError(code, "rlt_paged_append")
         return q_out
 
     def paged_attention(self, batch: PagedBatch, pool: torch.Tensor, q: torch.Tensor, out: torch.Tensor | None = None,
@@ -470,36 +491,42 @@ class RLTModel:
         """rlt_paged_attention: q [N, n_heads, head_dim] (rotated, the model's dtype) over the pool, which
         holds the new tokens already -> out, the same shape (rows behind the last sequence are left as
         they were).  scale 0: 1 / sqrt(head_dim)."""
-        ref = self._pool(batch, pool)
-        H = q.shape[1]
-        _need(q, "q", self.sdtype, self.device, (batch.N, None, self.cfg.head_dim))
+        ref = self._paged(batch, pool)
+        H, dev = q.shape[1], self._dev
+        shape = (batch.N, H, self.cfg.head_dim)
+        _need(q, "q", self.sdtype, dev, shape)
         if out is None:
-            out = torch.empty((batch.N, H, self.cfg.head_dim), dtype=self.sdtype, device=self.device)
-        _need(out, "out", self.sdtype, self.device, (batch.N, H, self.cfg.head_dim))
+            out = torch.empty(shape, dtype=self.sdtype, device=self.device)
+        else:
+            _need(out, "out", self.sdtype, dev, shape)
         # the workspace is the caller's stream's: from torch's allocator, for this call alone
-        nb = lib().rlt_paged_attention_workspace_bytes(self.handle, ref, H)
+        nb = batch.attention_workspace_bytes(H)
         ws = torch.empty(nb, dtype=torch.uint8, device=self.device) if nb else None
-        _check(lib().rlt_paged_attention(self.handle, ref, pool.data_ptr(), q.data_ptr(), _row_stride(q, "q"), H,
-                                         out.data_ptr(), _row_stride(out, "out"), float(scale), _ptr(ws), nb,
-                                         _stream()), "rlt_paged_attention")
+        code = lib().rlt_paged_attention(self.handle, ref, pool.data_ptr(), q.data_ptr(), _row_stride(q, "q"), H,
+                                         out.data_ptr(), _row_stride(out, "out"), scale,
+                                         None if ws is None else ws.data_ptr(), nb, self._raw_stream())
+        if code:
+            raise RLTError(code, "rlt_paged_attention")
         return out
 
     def encode_chunk(self, batch: PagedBatch, pools: torch.Tensor, tokens: torch.Tensor, e: torch.Tensor,
                      M: torch.Tensor) -> None:
         """rlt_encode_chunk: encode tokens int32 [N] over pools (alloc_pages); the new rows of e
         [B, T_alloc, d] and M [G, 2, B, n_heads, T_alloc, head_dim] are written in place."""
-        c = self.cfg
-        _need(pools, "pools", self.sdtype, self.device, (c.L_E, None, 2, c.n_heads, batch.page_size, c.head_dim))
-        ref = self._pool(batch, pools[0])
-        _need(tokens, "tokens", torch.int32, self.device, (batch.N,))
-        _need(e, "e", self.sdtype, self.device, (batch.B, None, c.d))
-        _need(M, "M", self.sdtype, self.device, (c.G, 2, batch.B, c.n_heads, e.shape[1], c.head_dim))
-        if not (pools.is_contiguous() and tokens.is_contiguous() and e.is_contiguous() and M.is_contiguous()):
-            raise ValueError("pools, tokens, e and M must be contiguous")
+        c, dev = self.cfg, self._dev
+        if pools.shape[0] != c.L_E or pools.dim() != 6 or not pools.is_contiguous():
+            raise ValueError(f"pools: need {c.L_E} pools, contiguous, got {list(pools.shape)}")
+        ref = self._paged(batch, pools[0])
+        T_alloc = e.shape[1]
+        _need(tokens, "tokens", torch.int32, dev, (batch.N,))
+        _need(e, "e", self.sdtype, dev, (batch.B, T_alloc, c.d))
+        _need(M, "M", self.sdtype, dev, (c.G, 2, batch.B, c.n_heads, T_alloc, c.head_dim))
+        if not (tokens.is_contiguous() and e.is_contiguous() and M.is_contiguous()):
+            raise ValueError("tokens, e and M must be contiguous")
         nb = lib().rlt_encode_chunk_workspace_bytes(self.handle, ref)
         ws = torch.empty(max(nb, 256), dtype=torch.uint8, device=self.device)
-        _check(lib().rlt_encode_chunk(self.handle, ref, _ptr(tokens), _ptr(pools), _ptr(e), _ptr(M), e.shape[1],
-                                      _ptr(ws), nb, _stream()), "rlt_encode_chunk")
+        _check(lib().rlt_encode_chunk(self.handle, ref, tokens.data_ptr(), pools.data_ptr(), e.data_ptr(), M.data_ptr(),
+                                      T_alloc, ws.data_ptr(), nb, self._raw_stream()), "rlt_encode_chunk")
 
     # ---------------------------------------------------------------- logits before a draw
     def process_logits(self, logits: torch.Tensor, *, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
@@ -513,45 +540,57 @@ class RLTModel:
         [B or 1, ceil(V / 32)] of allowed bits, per-row float32 parameters; returns out, the
         log-probabilities that sample() draws from.  With lse, logits are log-probabilities at
         temperature 1.  out may be logits."""
-        B, V = logits.shape[0], self.cfg.V
-        dev = self.device
-        _need(logits, "logits", torch.float32, dev, (B, V))
-        out = torch.empty((B, V), dtype=torch.float32, device=dev) if out is None else out
-        _need(out, "out", torch.float32, dev, (B, V))
+        B, V, dev, f32 = logits.shape[0], self.cfg.V, self._dev, torch.float32
+        _need(logits, "logits", f32, dev, (B, V))
+        if out is None:
+            out = torch.empty((B, V), dtype=f32, device=self.device)
+        else:
+            _need(out, "out", f32, dev, (B, V))
+        xs, os = logits.stride(), out.stride()
+        if xs[1] != 1 or os[1] != 1:
+            raise ValueError("the rows of logits and out must be contiguous")
         a = LogitsArgs()
-
-        def rows(t, what, dtype, n):
-            if t.shape[0] != 1:
-                _need(t, what, dtype, dev, (B, n))
-            else:
-                _need(t, what, dtype, dev, (1, n))
-            if t.stride(1) != 1 and n > 1:
-                raise ValueError(f"{what}: rows must be contiguous")
-            return t.stride(0) if t.shape[0] > 1 else (0 if what in ("bias", "mask") else n)
-
-        a.x, a.x_stride = logits.data_ptr(), rows(logits, "logits", torch.float32, V)
-        a.out, a.out_stride = out.data_ptr(), rows(out, "out", torch.float32, V)
+        a.x, a.x_stride = logits.data_ptr(), xs[0] if B > 1 else V
+        a.out, a.out_stride = out.data_ptr(), os[0] if B > 1 else V
         if bias is not None:
-            a.bias, a.bias_stride = bias.data_ptr(), rows(bias, "bias", torch.float32, V)
+            a.bias, a.bias_stride = self._broadcast_rows(bias, "bias", f32, B, V)
         if mask is not None:
-            a.mask, a.mask_stride = mask.data_ptr(), rows(mask, "mask", torch.int32, (V + 31) // 32)
+            a.mask, a.mask_stride = self._broadcast_rows(mask, "mask", torch.int32, B, (V + 31) // 32)
         if tokens is not None:
-            _need(tokens, "tokens", torch.int32, dev, (B, None))
-            a.tokens, a.n_tokens = tokens.data_ptr(), tokens.shape[1]
+            n = tokens.shape[1]
+            _need(tokens, "tokens", torch.int32, dev, (B, n))
+            a.tokens, a.n_tokens = tokens.data_ptr(), n
             a.seq_stride, a.tok_stride = tokens.stride()
+            a.tok_len = self._row_vector(tok_len, "tok_len", torch.int32, B)
+            a.gen_start = self._row_vector(gen_start, "gen_start", torch.int32, B)
         elif tok_len is not None or gen_start is not None:
             raise ValueError("tok_len and gen_start belong to tokens")
-        for name, t, dtype in (("lse", lse, torch.float32), ("tok_len", tok_len, torch.int32),
-                               ("gen_start", gen_start, torch.int32), ("repetition", repetition, torch.float32),
-                               ("presence", presence, torch.float32), ("frequency", frequency, torch.float32),
-                               ("tau", tau, torch.float32), ("out_lse", out_lse, torch.float32)):
-            if t is not None:
-                _need(t, name, dtype, dev, (B,))
-                if not t.is_contiguous():
-                    raise ValueError(f"{name}: must be contiguous")
-                setattr(a, name, t.data_ptr())
-        _check(lib().rlt_process_logits(self.handle, ctypes.byref(a), B, _stream()), "rlt_process_logits")
+        a.lse = self._row_vector(lse, "lse", f32, B)
+        a.repetition = self._row_vector(repetition, "repetition", f32, B)
+        a.presence = self._row_vector(presence, "presence", f32, B)
+        a.frequency = self._row_vector(frequency, "frequency", f32, B)
+        a.tau = self._row_vector(tau, "tau", f32, B)
+        a.out_lse = self._row_vector(out_lse, "out_lse", f32, B)
+        code = lib().rlt_process_logits(self.handle, ctypes.byref(a), B, self._raw_stream())
+        if code:
+            raise RLTError(code, "rlt_process_logits")
         return out
+
+    def _row_vector(self, t: torch.Tensor | None, what: str, dtype, B: int):
+        if t is None:
+            return None
+        _need(t, what, dtype, self._dev, (B,))
+        if B > 1 and t.stride(0) != 1:
+            raise ValueError(f"{what}: must be contiguous")
+        return t.data_ptr()
+
+    def _broadcast_rows(self, t: torch.Tensor, what: str, dtype, B: int, n: int):
+        """(address, row stride) of [B, n], or of [1, n] with a stride of 0."""
+        rows = 1 if t.shape[0] == 1 else B
+        _need(t, what, dtype, self._dev, (rows, n))
+        if n > 1 and t.stride(1) != 1:
+            raise ValueError(f"{what}: rows must be contiguous")
+        return t.data_ptr(), t.stride(0) if rows > 1 else 0
 
     def generate(self, prompt: torch.Tensor, n_new: int, uniforms: torch.Tensor, tau: float = 1.0, top_k: int = 0,
                  top_p: float = 1.0, *, repetition=None, presence=None, frequency=None,
