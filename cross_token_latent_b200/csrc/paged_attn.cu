@@ -5,6 +5,7 @@
 // group are taken together (rows are numbered i * g + j), so that shared keys are read once; a
 // long key axis is cut into units (paged.cuh) whose partial states k_paged_join merges.
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace rlt {
 
@@ -261,14 +262,17 @@ __global__ void __launch_bounds__(128) k_paged_simt(PagedArgs p, PagedAttnArgs a
 
 // ------------------------------------------------------------------ few rows, tensor cores
 // 16 rows of one key head against groups of 16 keys that the warps take in turn, on
-// mma.m16n8k16, keys and values straight from memory to the fragments.  What bounds it is
-// reading the keys and values once; a tile's 16 rows are mostly empty in a decode step, and the
-// warp-level product needs no staging, no tensor memory and no barrier on the way.
+// mma.m16n8k16.  What bounds it is reading the keys and values once; a tile's 16 rows are mostly
+// empty in a decode step, and the warp-level product needs no tensor memory and no barrier between
+// warps on the way.  A group lies in one page, 16 head_dim elements side by side for the keys and
+// again for the values, so each warp has them copied whole (cp.async.bulk) into a ring of its own,
+// several groups ahead; loading the fragments straight from memory left too few bytes in flight
+// beside the accumulators (64 ragged contexts, 1.1 GB: 220 us, 77 % of the copy rate).
 //
 // The contraction over head_dim may run in any order, so lane t of a quad takes 8 consecutive
-// elements of its key (one 16-byte load) and the queries are loaded to match; columns of the
-// output are dealt so that a lane reads 16 consecutive bytes of a value and ends up with
-// consecutive output columns.
+// elements of its key (16 bytes) and the queries are loaded to match; columns of the output are
+// dealt so that a lane reads 16 consecutive bytes of a value and ends up with consecutive output
+// columns.
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -280,12 +284,9 @@ __device__ __forceinline__ float ex2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// W consecutive 32-bit words (zeros where ok is false)
+// W consecutive 32-bit words
 template <int W>
-__device__ __forceinline__ void load_words(const bf16* p, bool ok, uint32_t* r) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) r[i] = 0;
-    if (!ok) return;
+__device__ __forceinline__ void load_words(const void* p, uint32_t* r) {
     if (W == 1) r[0] = *reinterpret_cast<const uint32_t*>(p);
     if (W == 2) {
         const uint2 x = *reinterpret_cast<const uint2*>(p);
@@ -306,197 +307,232 @@ struct MmaShape {
     static constexpr int VP = HD >= 64 ? HD / 64 : 1;
     static constexpr int NT = HD / 8;                       // output tiles of 8 columns
     static constexpr int LD = HD + 4;
-    static constexpr int SMEM = MMA_WARPS * 16 * LD * 4;
-    static constexpr int CTAS = HD == 128 ? 2 : (HD == 64 ? 4 : 5);      // resident per SM
+    static constexpr int GROUP = 16 * HD * 2;               // bytes of a group's keys, and of its values
+    // Stages of a warp's ring, CTAs per SM: 192 KB in flight at head widths of 128 and 64.  (At 128, two
+    // CTAs with three stages take 193 us for the 64 contexts where three with two take 182 us.)
+    static constexpr int STAGES = HD == 128 ? 2 : (HD == 64 ? 3 : 4);
+    static constexpr int CTAS = HD == 128 ? 3 : (HD == 64 ? 4 : 5);
+    static constexpr int RING = MMA_WARPS * STAGES * 2 * GROUP;
+    static constexpr int JOIN = MMA_WARPS * 16 * LD * 4;    // over the rings, when they are through
+    static constexpr int SMEM = RING > JOIN ? RING : JOIN;
 };
 
 template <int HD>
-__global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mma(PagedArgs p, PagedAttnArgs a, UnitPlan u, int units) {
+__global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mma(PagedArgs p, PagedAttnArgs a, UnitPlan u,
+                                                                                  int units) {
     using S = MmaShape<HD>;
-    extern __shared__ __align__(16) float sm[];             // [warps][16][LD]: accumulators, maximum, sum
+    extern __shared__ __align__(128) uint8_t ring_sm[];     // [warps][STAGES][keys, values]
+    float* sm = reinterpret_cast<float*>(ring_sm);          // [warps][16][LD]: accumulators, maximum, sum
+    __shared__ uint64_t full[MMA_WARPS][S::STAGES];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    if (lane == 0) {
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(&full[warp][i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
     pdl_wait();
     pdl_trigger();
-    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    Unit w;
-    if (!find_unit(p, u, unit, false, w)) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int row0 = w.tile * 16, rows = min(16, w.s.nq * u.g - row0), ctx = w.s.kv - w.s.nq;
-    const int last = ctx + (row0 + rows - 1) / u.g;
-    const int k_begin = w.split * w.chunk, k_end = min(last + 1, k_begin + w.chunk);
-    if (k_begin >= k_end) continue;
+    uint8_t* ring = ring_sm + warp * S::STAGES * 2 * S::GROUP;
+    int stage = 0;                                          // of the next group to be computed
+    uint32_t phase = 0;
     const float c2 = a.scale * LOG2E;
-
-    uint32_t q[2][S::QP][S::QW];
-    int limit[2];                                           // the last key of rows g and g + 8
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = row0 + g + 8 * i, tok = row / u.g;
-        const bool ok = g + 8 * i < rows;
-        limit[i] = ok ? ctx + tok : -1;
-        const bf16* qp = reinterpret_cast<const bf16*>(a.q) + (long long)(w.s.q0 + tok) * a.q_stride +
-                         (long long)(w.head * u.g + row % u.g) * HD;
-#pragma unroll
-        for (int c = 0; c < S::QP; ++c) load_words<S::QW>(qp + (c * 4 + t) * S::QW * 2, ok, q[i][c]);
-    }
-
-    float m[2] = {NEG_BIG, NEG_BIG}, l[2] = {0.f, 0.f};     // m of the scores as they are
-    float o[S::NT][4];
-#pragma unroll
-    for (int j = 0; j < S::NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-
     const bf16* pool = reinterpret_cast<const bf16*>(a.pool);
     const long long head_elems = (long long)HD << p.page_shift, v_off = p.Hkv * head_elems;
     const int page_mask = (1 << p.page_shift) - 1;
-    // this warp's groups: keys k_begin + 16 (warp + 4 i); lane j keeps the page of group i0 + j
-    const int n_groups = (k_end - k_begin + 15) / 16;
-    const int mine = n_groups > warp ? (n_groups - warp + MMA_WARPS - 1) / MMA_WARPS : 0;
-    auto key0 = [&](int i) { return k_begin + 16 * (warp + MMA_WARPS * i); };
-    int pages = 0;
-    auto load_pages = [&](int i0) {
-        const int i = i0 + lane;
-        pages = i < mine ? max(load_page(p, w.b, key0(i)), 0) : 0;
-    };
-    auto base = [&](int i) {
-        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-        return pool + ((long long)page * 2 * p.Hkv + w.head) * head_elems + (long long)(key0(i) & page_mask) * HD;
-    };
-    uint32_t kf[2][S::QP][S::QW], vf[4][S::VP][S::VW];
-    auto load_k = [&](const bf16* kp, int i) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int c = 0; c < S::QP; ++c)
-                load_words<S::QW>(kp + (long long)(8 * n + g) * HD + (c * 4 + t) * S::QW * 2, key0(i) + 8 * n + g < k_end,
-                                  kf[n][c]);
-    };
-    auto load_v = [&](const bf16* vp, int i) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int j = 2 * t + (n & 1) + 8 * (n >> 1);   // keys 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-            for (int c = 0; c < S::VP; ++c)
-                load_words<S::VW>(vp + (long long)j * HD + (c * 8 + g) * S::VW * 2, key0(i) + j < k_end, vf[n][c]);
-        }
-    };
 
-    if (mine > 0) {
-        load_pages(0);
-        const bf16* kp = base(0);
-        load_k(kp, 0);
-        load_v(kp + v_off, 0);
-    }
-    for (int i = 0; i < mine; ++i) {
-        float s[2][4] = {};
-#pragma unroll
-        for (int c = 0; c < S::QP; ++c)
-#pragma unroll
-            for (int h = 0; h < S::QW; h += 2) {
-                const uint32_t af[4] = {q[0][c][h], q[1][c][h], q[0][c][h + 1], q[1][c][h + 1]};
-#pragma unroll
-                for (int n = 0; n < 2; ++n) mma16816(s[n], af, kf[n][c][h], kf[n][c][h + 1]);
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        Unit w;
+        if (!find_unit(p, u, unit, false, w)) return;
+        const int row0 = w.tile * 16, rows = min(16, w.s.nq * u.g - row0), ctx = w.s.kv - w.s.nq;
+        const int last = ctx + (row0 + rows - 1) / u.g;
+        const int k_begin = w.split * w.chunk, k_end = min(last + 1, k_begin + w.chunk);
+        if (k_begin >= k_end) continue;
+
+        // this warp's groups: keys k_begin + 16 (warp + 4 i); lane j keeps the page of group i0 + j
+        const int n_groups = (k_end - k_begin + 15) / 16;
+        const int mine = n_groups > warp ? (n_groups - warp + MMA_WARPS - 1) / MMA_WARPS : 0;
+        auto key0 = [&](int i) { return k_begin + 16 * (warp + MMA_WARPS * i); };
+        int pages = 0, fill = stage;                        // fill: stage of the next group to be copied
+        auto copy = [&](int i) {
+            if ((i & 31) == 0) pages = i + lane < mine ? max(load_page(p, w.b, key0(i + lane)), 0) : 0;
+            const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+            if (lane == 0) {
+                const bf16* src = pool + ((long long)page * 2 * p.Hkv + w.head) * head_elems +
+                                  (long long)(key0(i) & page_mask) * HD;
+                uint8_t* dst = ring + fill * 2 * S::GROUP;
+                mbar_expect_tx(&full[warp][fill], 2 * S::GROUP);
+                bulk_load(dst, src, S::GROUP, &full[warp][fill]);
+                bulk_load(dst + S::GROUP, src + v_off, S::GROUP, &full[warp][fill]);
             }
-        // the next group's keys are under way while this one's softmax runs
-        const bf16* kp = nullptr;
-        if (i + 1 < mine) {
-            if (((i + 1) & 31) == 0) load_pages(i + 1);
-            kp = base(i + 1);
-            load_k(kp, i + 1);
+            if (++fill == S::STAGES) fill = 0;
+        };
+        for (int i = 0; i < S::STAGES && i < mine; ++i) copy(i);
+
+        uint32_t q[2][S::QP][S::QW];
+        int limit[2];                                       // the last key of rows g and g + 8
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = row0 + g + 8 * i, tok = row / u.g;
+            const bool ok = g + 8 * i < rows;
+            limit[i] = ok ? ctx + tok : -1;
+            const bf16* qp = reinterpret_cast<const bf16*>(a.q) + (long long)(w.s.q0 + tok) * a.q_stride +
+                             (long long)(w.head * u.g + row % u.g) * HD;
+#pragma unroll
+            for (int c = 0; c < S::QP; ++c) {
+#pragma unroll
+                for (int e = 0; e < S::QW; ++e) q[i][c][e] = 0;
+                if (ok) load_words<S::QW>(qp + (c * 4 + t) * S::QW * 2, q[i][c]);
+            }
         }
-        const int k0 = key0(i);
-        float mx[2] = {m[0], m[1]};
+
+        float m[2] = {NEG_BIG, NEG_BIG}, l[2] = {0.f, 0.f};     // m of the scores as they are
+        float o[S::NT][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int j = 0; j < S::NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (k0 + 8 * n + 2 * t + (e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
-                mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+
+        bool ok = true;
+        for (int i = 0; i < mine; ++i) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][stage], phase, nullptr));
+            if (!ok) break;
+            const uint8_t* kb = ring + stage * 2 * S::GROUP;
+            float s[2][4] = {};
+#pragma unroll
+            for (int c = 0; c < S::QP; ++c) {
+                uint32_t kf[2][S::QW];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) load_words<S::QW>(kb + (8 * n + g) * HD * 2 + (c * 4 + t) * S::QW * 4, kf[n]);
+#pragma unroll
+                for (int h = 0; h < S::QW; h += 2) {
+                    const uint32_t af[4] = {q[0][c][h], q[1][c][h], q[0][c][h + 1], q[1][c][h + 1]};
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) mma16816(s[n], af, kf[n][h], kf[n][h + 1]);
+                }
             }
+            const int k0 = key0(i);
+            float mx[2] = {m[0], m[1]};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (k0 + 8 * n + 2 * t + (e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
+                    mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
+                }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            }
+            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float al = ex2_approx((m[r] - mx[r]) * c2);
+                    l[r] *= al;
+                    m[r] = mx[r];
+#pragma unroll
+                    for (int j = 0; j < S::NT; ++j) { o[j][2 * r] *= al; o[j][2 * r + 1] *= al; }
+                }
+            }
+            // probabilities rounded to bf16 for the product; the sum is of the rounded values, so that
+            // the result stays a weighted mean of the values
+            uint32_t pf[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float mc = m[r] == NEG_BIG ? 0.f : m[r] * c2;
+                    __nv_bfloat162 h = __floats2bfloat162_rn(ex2_approx(fmaf(s[n][2 * r], c2, -mc)),
+                                                             ex2_approx(fmaf(s[n][2 * r + 1], c2, -mc)));
+                    const uint32_t x = *reinterpret_cast<uint32_t*>(&h);
+                    l[r] += __uint_as_float(x << 16) + __uint_as_float(x & 0xffff0000u);
+                    pf[2 * n + r] = x;
+                }
+#pragma unroll
+            for (int c = 0; c < S::VP; ++c) {
+                uint32_t vf[4][S::VW];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int j = 2 * t + (n & 1) + 8 * (n >> 1);       // keys 2t, 2t + 1, 2t + 8, 2t + 9
+                    load_words<S::VW>(kb + S::GROUP + j * HD * 2 + (c * 8 + g) * S::VW * 4, vf[n]);
+                    if (k0 + 16 > k_end) {
+                        // slots behind the last key hold anything, and 0 * NaN is NaN
+#pragma unroll
+                        for (int e = 0; e < S::VW; ++e) vf[n][e] = k0 + j < k_end ? vf[n][e] : 0u;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < S::VW; ++e) {
+                    mma16816(o[(c * S::VW + e) * 2], pf, __byte_perm(vf[0][e], vf[1][e], 0x5410),
+                             __byte_perm(vf[2][e], vf[3][e], 0x5410));
+                    mma16816(o[(c * S::VW + e) * 2 + 1], pf, __byte_perm(vf[0][e], vf[1][e], 0x7632),
+                             __byte_perm(vf[2][e], vf[3][e], 0x7632));
+                }
+            }
+            __syncwarp();                                   // the stage is read
+            if (++stage == S::STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+            if (i + S::STAGES < mine) copy(i + S::STAGES);
+        }
+        if (!ok && lane == 0) {
+            raise_flag(p.hdr, ERR_TIMEOUT);
+            // the copies in flight land before the shared memory is given back
+            for (int i = 0; i < S::STAGES; ++i) {
+                if (mine > i) mbar_wait(&full[warp][stage], phase, nullptr);
+                if (++stage == S::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+
+        // Join the warps.  Lane t of quad g has, of piece c, columns (c * 8 + 2t) * 2 VW .. + 4 VW - 1:
+        // tile j's element 0 is column (c * 8 + 2t) * 2 VW + j, element 1 is 2 VW further.
+        if (__syncthreads_or(!ok)) return;                  // (behind it the rings are through)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        }
-        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            float* dst = sm + (warp * 16 + g + 8 * r) * S::LD;
+            if (g + 8 * r < rows) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float al = ex2_approx((m[r] - mx[r]) * c2);
-                l[r] *= al;
-                m[r] = mx[r];
+                for (int c = 0; c < S::VP; ++c)
 #pragma unroll
-                for (int j = 0; j < S::NT; ++j) { o[j][2 * r] *= al; o[j][2 * r + 1] *= al; }
+                    for (int e = 0; e < 2 * S::VW; ++e) {
+                        dst[(c * 8 + 2 * t) * 2 * S::VW + e] = o[c * S::VW * 2 + e][2 * r];
+                        dst[(c * 8 + 2 * t + 1) * 2 * S::VW + e] = o[c * S::VW * 2 + e][2 * r + 1];
+                    }
+                if (t == 0) { dst[HD] = m[r] * c2; dst[HD + 1] = l[r]; }
             }
         }
-        // probabilities rounded to bf16 for the product; the sum is of the rounded values, so that
-        // the result stays a weighted mean of the values
-        uint32_t pf[4];
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * HD; i += MMA_WARPS * 32) {
+            const int r = i / HD, col = i % HD;
+            float mt = NEG_BIG;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+            for (int x = 0; x < MMA_WARPS; ++x) mt = fmaxf(mt, sm[(x * 16 + r) * S::LD + HD]);
+            float lt = 0.f, acc = 0.f;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float mc = m[r] == NEG_BIG ? 0.f : m[r] * c2;
-                __nv_bfloat162 h = __floats2bfloat162_rn(ex2_approx(fmaf(s[n][2 * r], c2, -mc)),
-                                                         ex2_approx(fmaf(s[n][2 * r + 1], c2, -mc)));
-                const uint32_t x = *reinterpret_cast<uint32_t*>(&h);
-                l[r] += __uint_as_float(x << 16) + __uint_as_float(x & 0xffff0000u);
-                pf[2 * n + r] = x;
+            for (int x = 0; x < MMA_WARPS; ++x) {
+                const float* src = sm + (x * 16 + r) * S::LD;
+                const float f = ex2_approx(src[HD] - mt);
+                lt += f * src[HD + 1];
+                acc += f * src[col];
             }
-#pragma unroll
-        for (int c = 0; c < S::VP; ++c)
-#pragma unroll
-            for (int e = 0; e < S::VW; ++e) {
-                mma16816(o[(c * S::VW + e) * 2], pf, __byte_perm(vf[0][c][e], vf[1][c][e], 0x5410),
-                         __byte_perm(vf[2][c][e], vf[3][c][e], 0x5410));
-                mma16816(o[(c * S::VW + e) * 2 + 1], pf, __byte_perm(vf[0][c][e], vf[1][c][e], 0x7632),
-                         __byte_perm(vf[2][c][e], vf[3][c][e], 0x7632));
+            if (w.n_splits > 1) {
+                float* pr = part_row(a, u, w.slot, r, HD);
+                pr[col] = acc;
+                if (col == 0) { pr[HD] = mt; pr[HD + 1] = lt; }
+            } else {
+                const int row = row0 + r;
+                reinterpret_cast<bf16*>(a.o)[(long long)(w.s.q0 + row / u.g) * a.o_stride +
+                                             (long long)(w.head * u.g + row % u.g) * HD + col] = from_f<bf16>(acc / lt);
             }
-        if (i + 1 < mine) load_v(kp + v_off, i + 1);
-    }
-
-    // Join the warps.  Lane t of quad g has, of piece c, columns (c * 8 + 2t) * 2 VW .. + 4 VW - 1:
-    // tile j's element 0 is column (c * 8 + 2t) * 2 VW + j, element 1 is 2 VW further.
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        float* dst = sm + (warp * 16 + g + 8 * r) * S::LD;
-        if (g + 8 * r < rows) {
-#pragma unroll
-            for (int c = 0; c < S::VP; ++c)
-#pragma unroll
-                for (int e = 0; e < 2 * S::VW; ++e) {
-                    dst[(c * 8 + 2 * t) * 2 * S::VW + e] = o[c * S::VW * 2 + e][2 * r];
-                    dst[(c * 8 + 2 * t + 1) * 2 * S::VW + e] = o[c * S::VW * 2 + e][2 * r + 1];
-                }
-            if (t == 0) { dst[HD] = m[r] * c2; dst[HD + 1] = l[r]; }
         }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * HD; i += MMA_WARPS * 32) {
-        const int r = i / HD, col = i % HD;
-        float mt = NEG_BIG;
-#pragma unroll
-        for (int x = 0; x < MMA_WARPS; ++x) mt = fmaxf(mt, sm[(x * 16 + r) * S::LD + HD]);
-        float lt = 0.f, acc = 0.f;
-#pragma unroll
-        for (int x = 0; x < MMA_WARPS; ++x) {
-            const float* src = sm + (x * 16 + r) * S::LD;
-            const float f = ex2_approx(src[HD] - mt);
-            lt += f * src[HD + 1];
-            acc += f * src[col];
-        }
-        if (w.n_splits > 1) {
-            float* pr = part_row(a, u, w.slot, r, HD);
-            pr[col] = acc;
-            if (col == 0) { pr[HD] = mt; pr[HD + 1] = lt; }
-        } else {
-            const int row = row0 + r;
-            reinterpret_cast<bf16*>(a.o)[(long long)(w.s.q0 + row / u.g) * a.o_stride +
-                                         (long long)(w.head * u.g + row % u.g) * HD + col] = from_f<bf16>(acc / lt);
-        }
-    }
-    __syncthreads();
+        fence_proxy_async_smem();                           // the next unit's copies come behind these accesses
+        __syncthreads();
     }
 }
 
@@ -535,7 +571,7 @@ Bf16Plans bf16_plans(const PagedArgs& p, int H, int hd) {
            (((long long)p.n_pages * 2 * p.Hkv) << p.page_shift) < (1LL << 31);
     PagedArgs few = p;              // its bounds
     if (b.tc) few.max_q = FEW_ROWS / g < 1 ? 1 : FEW_ROWS / g;
-    b.u_mma = make_plan(few, H, 16, 1, b.tc ? FEW_ROWS : ANY, 256, 64, 148 * 12);
+    b.u_mma = make_plan(few, H, 16, 1, b.tc ? FEW_ROWS : ANY, 256, 64, 148 * 9);
     b.floats = (size_t)b.u_mma.slots * b.u_mma.rt * (hd + 2);
     b.u_tc = {};
     if (b.tc) {
@@ -559,11 +595,13 @@ Bf16Plans bf16_plans(const PagedArgs& p, int H, int hd) {
 
 template <int HD>
 cudaError_t run_mma(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u, long long items, bool beside_tc) {
-    // A block per unit (592 blocks that walk through the units took 249 us for 64 decode contexts where
-    // this takes 220), but where another kernel has the long sequences there may be few units or none,
-    // and then blocks that look for theirs in vain cost more: no more than are resident at once.
+    // A block per unit: blocks that walk through the units took 13 % longer for 64 decode contexts.  But
+    // where another kernel has the long sequences there may be few units or none, and then blocks that
+    // look for theirs in vain cost more: no more than are resident at once.
     const int units = (int)(items + (u.slots ? u.target : 0));
     const int most = sm_count() * MmaShape<HD>::CTAS, grid = beside_tc && units > most ? most : units;
+    cudaError_t e = cudaFuncSetAttribute(k_paged_mma<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaShape<HD>::SMEM);
+    if (e != cudaSuccess) return e;
     return launch_k(L, k_paged_mma<HD>, (unsigned)grid, MMA_WARPS * 32, MmaShape<HD>::SMEM, p, a, u, units);
 }
 
