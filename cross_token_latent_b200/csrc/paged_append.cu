@@ -46,57 +46,69 @@ __device__ __forceinline__ void store_vec(bf16* p, const float* x) {
 }
 
 // A work item is VEC elements f .. of a head's lower half together with their partners in the
-// upper half; the items of a row are its query heads', its key heads', its value heads'.
+// upper half; the items of a row are its query heads', its key heads', its value heads'.  A thread
+// has the same item of every row it walks through, so that only the row's place is to be looked up,
+// and its elements of the next row are on their way meanwhile: where they come from depends on the
+// row's number alone.
 template <typename T, typename S, int VEC>
 __global__ void __launch_bounds__(256) k_paged_append(PagedArgs p, AppendArgs a) {
     pdl_wait();
     pdl_trigger();
     const int half = a.hd / 2, per_head = half / VEC;
-    const int items = (a.H + 2 * p.Hkv) * per_head;
-    const int chunks = (items + blockDim.x - 1) / blockDim.x;       // of a row, one per block
-    const long long blocks = (long long)p.N * chunks;
-    for (long long w = blockIdx.x; w < blocks; w += gridDim.x) {
-        const int r = (int)(w / chunks);
-        const int i = (int)(w % chunks) * blockDim.x + threadIdx.x;
-        if (i >= items) continue;
-        const int b = find_seq(p, r);
-        if (b < 0) continue;
-        const Seq s = load_seq(p, b);
-        if (r >= s.q0 + s.nq) continue;                             // a row behind the last sequence
-        const int pos = s.kv - s.nq + (r - s.q0);
-        const int head = i / per_head, f = (i % per_head) * VEC;
-        float lo[VEC], hi[VEC];
-        const S* src;
-        T* dst;
-        if (head < a.H) {
-            src = reinterpret_cast<const S*>(a.q) + r * a.q_stride + (long long)head * a.hd;
-            dst = reinterpret_cast<T*>(a.q_out) + r * a.q_out_stride + (long long)head * a.hd;
-        } else {
-            const int h = head - a.H, kv = h >= p.Hkv, hk = kv ? h - p.Hkv : h;
-            src = (kv ? reinterpret_cast<const S*>(a.v) + r * a.v_stride
-                      : reinterpret_cast<const S*>(a.k) + r * a.k_stride) + (long long)hk * a.hd;
-            const int page = load_page(p, b, pos);
-            if (page < 0) continue;
-            const int slot = pos & ((1 << p.page_shift) - 1);
-            dst = reinterpret_cast<T*>(a.pool) +
-                  (((((long long)page * 2 + kv) * p.Hkv + hk) << p.page_shift) + slot) * a.hd;
+    const int i = blockIdx.y * blockDim.x + threadIdx.x;
+    if (i >= (a.H + 2 * p.Hkv) * per_head) return;
+    const int head = i / per_head, f = (i % per_head) * VEC, h = head - a.H;
+    const bool is_q = head < a.H, is_v = h >= p.Hkv;
+    const int hk = is_v ? h - p.Hkv : h;
+    const long long stride = is_q ? a.q_stride : (is_v ? a.v_stride : a.k_stride);
+    const S* src = reinterpret_cast<const S*>(is_q ? a.q : (is_v ? a.v : a.k)) + (long long)(is_q ? head : hk) * a.hd + f;
+    T* const dst_q = reinterpret_cast<T*>(a.q_out) + (long long)head * a.hd + f;
+    T* const dst_kv = reinterpret_cast<T*>(a.pool) + f;
+    float lo[VEC], hi[VEC];
+    int r = blockIdx.x;
+    load_vec<VEC>(src + r * stride, lo);
+    load_vec<VEC>(src + r * stride + half, hi);
+    for (; r < p.N; r += gridDim.x) {
+        float next_lo[VEC], next_hi[VEC];
+        const int rn = r + gridDim.x;
+        if (rn < p.N) {
+            load_vec<VEC>(src + rn * stride, next_lo);
+            load_vec<VEC>(src + rn * stride + half, next_hi);
         }
-        load_vec<VEC>(src + f, lo);
-        load_vec<VEC>(src + f + half, hi);
-        if (head < a.H + p.Hkv) {
-            const float4* cs = reinterpret_cast<const float4*>(a.rope + (long long)pos * half + f);
+        const int b = find_seq(p, r);
+        Seq s = {0, 0, 0};
+        if (b >= 0) s = load_seq(p, b);
+        if (r < s.q0 + s.nq) {                          // no row behind the last sequence
+            const int pos = s.kv - s.nq + (r - s.q0);
+            T* dst = dst_q + r * a.q_out_stride;
+            bool ok = true;
+            if (!is_q) {
+                const int page = load_page(p, b, pos), slot = pos & ((1 << p.page_shift) - 1);
+                ok = page >= 0;
+                dst = dst_kv + (((((long long)page * 2 + is_v) * p.Hkv + hk) << p.page_shift) + slot) * a.hd;
+            }
+            if (!is_v) {
+                const float4* cs = reinterpret_cast<const float4*>(a.rope + (long long)pos * half + f);
 #pragma unroll
-            for (int j = 0; j < VEC; j += 2) {
-                const float4 t = __ldg(cs + j / 2);
-                const float x0 = lo[j], y0 = hi[j], x1 = lo[j + 1], y1 = hi[j + 1];
-                lo[j] = x0 * t.x - y0 * t.y;
-                hi[j] = x0 * t.y + y0 * t.x;
-                lo[j + 1] = x1 * t.z - y1 * t.w;
-                hi[j + 1] = x1 * t.w + y1 * t.z;
+                for (int j = 0; j < VEC; j += 2) {
+                    const float4 t = __ldg(cs + j / 2);
+                    const float x0 = lo[j], y0 = hi[j], x1 = lo[j + 1], y1 = hi[j + 1];
+                    lo[j] = x0 * t.x - y0 * t.y;
+                    hi[j] = x0 * t.y + y0 * t.x;
+                    lo[j + 1] = x1 * t.z - y1 * t.w;
+                    hi[j + 1] = x1 * t.w + y1 * t.z;
+                }
+            }
+            if (ok) {
+                store_vec<VEC>(dst, lo);
+                store_vec<VEC>(dst + half, hi);
             }
         }
-        store_vec<VEC>(dst + f, lo);
-        store_vec<VEC>(dst + f + half, hi);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            lo[j] = next_lo[j];
+            hi[j] = next_hi[j];
+        }
     }
 }
 
@@ -146,12 +158,15 @@ inline unsigned rows_grid(long long n) {
 
 }  // namespace
 
+constexpr int ROW_BLOCKS = 16;          // per SM (32768 rows, heads of 128: 8 take 223 us, 16 take 201 us)
+
 template <typename T, typename S>
 cudaError_t launch_paged_append(Launch L, const PagedArgs& p, const AppendArgs& a) {
-    // 8 elements of a half head per thread, 16 bytes and more each way; heads of 16 have halves of 8
-    const int items = (a.H + 2 * p.Hkv) * (a.hd / 16);
-    const long long blocks = (long long)p.N * ((items + 255) / 256);
-    return launch_k(L, k_paged_append<T, S, 8>, rows_grid(blocks), 256, 0, p, a);
+    // 16 bytes per load: 4 float32 elements, 8 in bf16 (heads of 16 have halves of 8)
+    constexpr int VEC = 16 / sizeof(S);
+    const int items = (a.H + 2 * p.Hkv) * (a.hd / (2 * VEC)), chunks = (items + 255) / 256;
+    const int most = (ROW_BLOCKS * sm_count() + chunks - 1) / chunks;
+    return launch_k(L, k_paged_append<T, S, VEC>, dim3(p.N < most ? p.N : most, chunks), 256, 0, p, a);
 }
 
 template <typename T>
