@@ -12,6 +12,7 @@
 //                that the compiler does not know to be alone took some 95 clocks per MMA).  A warp per
 //                stage was slower: their products interleave, both softmaxes fall in step and the
 //                tensor core idles meanwhile
+//   warp 10      clears the end of a last V tile
 // While one stage's rows are in the softmax the tensor core works on the other stage, and an item's
 // last products and its output overlap with the next one's first loads and scores.  The running
 // maximum moves only when it grew by more than 2^8 (RESCALE): a smaller maximum is as good a
@@ -46,8 +47,8 @@ struct TcShape {
     static constexpr uint32_t O_COL = STAGES * KH;          // O behind the scores
     static constexpr uint32_t TMEM_COLS = STAGES * (KH + HD);
     static constexpr int SOFTMAX_WARPS = 4 * STAGES;
-    static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 1;
-    static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
+    static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 1, CLEARER = SOFTMAX_WARPS + 2;
+    static constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
 };
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -262,8 +263,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     uint64_t* s_full = kv_empty + S::SLOTS;     // [stage] the next block's scores
     uint64_t* p_full = s_full + S::STAGES;      // [stage] its probabilities, O rescaled
     uint64_t* o_done = p_full + S::STAGES;      // [stage] an item's last product
-    uint64_t* tail_full = o_done + S::STAGES;          // a V tile whose end is to be cleared
-    uint64_t* drained = tail_full + 1;          // after a timeout: the MMAs issued have completed
+    uint64_t* tail_full = o_done + S::STAGES;   // [SLOTS] a V tile whose end is to be cleared
+    uint64_t* drained = tail_full + S::SLOTS;          // after a timeout: the MMAs issued have completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     __shared__ int abort_flag;
     __shared__ ShareSmem share_sm;
@@ -288,13 +289,13 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         for (int s = 0; s < S::SLOTS; ++s) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
+            mbar_init(&tail_full[s], 1);
         }
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
-        mbar_init(tail_full, 1);
         mbar_init(drained, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -339,20 +340,20 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 const int seen = limit - h * S::KH;         // columns 0 .. seen of this block are seen
                 const bool masked = __any_sync(0xffffffffu, seen < S::KH - 1);
                 float mx = -INFINITY;
-                // The scores are read twice, for the maximum and for the exponentials: keeping them would take
-                // registers that there are none of at this number of warps.
-                uint32_t x[2][32];
+                // Where two CTAs share the registers the scores are read twice, for the maximum and for the
+                // exponentials.
+                constexpr int KEEP = S::CTAS == 1 ? S::KH / 32 : 2;
+                uint32_t x[KEEP][32];
 #pragma unroll
-                for (int c = 0; c < S::KH / 32; c += 2) {
-                    tmem_ld32_async(t_s + 32 * c, x[0]);
-                    tmem_ld32_async(t_s + 32 * c + 32, x[1]);
-                    tmem_wait_ld(x[0]);
-                    tmem_wait_ld(x[1]);
-                    if (masked) {
-                        mask32(x[0], seen - 32 * c);
-                        mask32(x[1], seen - 32 * c - 32);
+                for (int c = 0; c < S::KH / 32; c += KEEP) {
+#pragma unroll
+                    for (int k = 0; k < KEEP; ++k) tmem_ld32_async(t_s + 32 * (c + k), x[k]);
+#pragma unroll
+                    for (int k = 0; k < KEEP; ++k) {
+                        tmem_wait_ld(x[k]);
+                        if (masked) mask32(x[k], seen - 32 * (c + k));
+                        mx = fmaxf(mx, max32(x[k]));
                     }
-                    mx = fmaxf(mx, fmaxf(max32(x[0]), max32(x[1])));
                 }
                 mx *= c2;
                 // (a first maximum needs no rescale: the first product overwrites O, and l is 0)
@@ -377,14 +378,13 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 // where columns are masked every exponential is exact at -inf
 #pragma unroll
                 for (int c = 0; c < S::KH / 32; ++c) {
-                    tmem_ld32_async(t_s + 32 * c, x[0]);
-                    tmem_wait_ld(x[0]);
-                    if (masked) {
-                        mask32(x[0], seen - 32 * c);
-                        l += softmax32<0>(x[0], t_s + 16 * c, c2, neg);
-                    } else {
-                        l += softmax32<S::POLY>(x[0], t_s + 16 * c, c2, neg);
+                    if (S::CTAS > 1) {
+                        tmem_ld32_async(t_s + 32 * c, x[0]);
+                        tmem_wait_ld(x[0]);
+                        if (masked) mask32(x[0], seen - 32 * c);
                     }
+                    const uint32_t(&xc)[32] = x[S::CTAS > 1 ? 0 : c];
+                    l += masked ? softmax32<0>(xc, t_s + 16 * c, c2, neg) : softmax32<S::POLY>(xc, t_s + 16 * c, c2, neg);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -438,7 +438,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             const int page_rows = min(KT, 1 << p.page_shift);
             const int pg = lane / S::ATOMS, atom = lane % S::ATOMS;
             Ring<S::SLOTS> ring;
-            uint32_t q_phase = 0, tail_phase = 0, items = 0;
+            uint32_t q_phase = 0, items = 0, tail_phases = 0, tails = 0;     // bits of slots: phases, last item a tail
             bool ok = true;
             do {
                 const Stretch<HD> x_(w, u);
@@ -464,27 +464,16 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                         ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[ring.slot], ring.phase ^ 1, &abort_flag));
                         if (!ok) break;
                         uint8_t* tile = smem + S::OFF_KV + ring.slot * S::T_BYTES;
+                        // (an item's last V tile may end inside: the clearing warp hands it on)
                         const bool tail = kv == 1 && have < KT;
-                        uint64_t* bar = tail ? tail_full : &kv_full[ring.slot];
+                        uint64_t* bar = tail ? &tail_full[ring.slot] : &kv_full[ring.slot];
                         if (lane == 0) mbar_expect_tx(bar, boxes * page_rows * 128);
                         __syncwarp();
                         if (mine)
                             tma_load_2d(tile + atom * KT * 128 + pg * page_rows * 128, &tmKV, bar, 64 * atom,
                                         (((page * 2 + kv) * p.Hkv + w.head) << p.page_shift) + in_page);
-                        if (tail) {
-                            // slots behind the last key hold anything, and 0 * NaN is NaN: they become zeros
-                            ok = __all_sync(0xffffffffu, mbar_wait(tail_full, tail_phase, &abort_flag));
-                            tail_phase ^= 1;
-                            if (!ok) break;
-                            for (int i = lane; i < (KT - have) * S::ATOMS * 8; i += 32) {
-                                const int piece = i & 7, at = (i >> 3) % S::ATOMS, r = have + (i >> 3) / S::ATOMS;
-                                *reinterpret_cast<uint4*>(tile + at * KT * 128 + r * 128 + piece * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&kv_full[ring.slot]);
-                        }
+                        tail_phases ^= (tail ? 1u : 0u) << ring.slot;
+                        tails = (tails & ~(1u << ring.slot)) | (tail ? 1u : 0u) << ring.slot;
                         ring.next();
                         ++items;
                     }
@@ -496,14 +485,40 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 // the copies in flight land before the shared memory is given back
                 if (lane == 0) {
                     mbar_wait(q_full, q_phase ^ 1, nullptr);
-                    mbar_wait(tail_full, tail_phase ^ 1, nullptr);
                     for (int i = 0; i < S::SLOTS && i < (int)items; ++i) {
-                        // the slot's last full round: behind the ring's position it is the round before
+                        // the slot's last round: behind the ring's position it is the round before
                         const uint32_t ph = i < ring.slot ? ring.phase : ring.phase ^ 1;
-                        mbar_wait(&kv_full[i], ph, nullptr);
+                        if (tails >> i & 1) mbar_wait(&tail_full[i], (tail_phases >> i & 1) ^ 1, nullptr);
+                        else mbar_wait(&kv_full[i], ph, nullptr);
                     }
                 }
             }
+        } else if (warp == S::CLEARER) {
+            // Slots behind a sequence's last key hold anything, and 0 * NaN is NaN: in the last V tile of an
+            // item that ends inside they become zeros before the tile is handed on.
+            int slot = 0;
+            uint32_t phases = 0;
+            bool ok = true;
+            do {
+                const Stretch<HD> x_(w, u);
+                const int have = x_.k_end - x_.k_begin - (x_.tiles - 1) * KT;
+                slot = (slot + 2 * x_.tiles - 1) % S::SLOTS;
+                if (have < KT) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&tail_full[slot], phases >> slot & 1, &abort_flag));
+                    if (!ok) break;
+                    phases ^= 1u << slot;
+                    uint8_t* tile = smem + S::OFF_KV + slot * S::T_BYTES;
+                    for (int i = lane; i < (KT - have) * S::ATOMS * 8; i += 32) {
+                        const int piece = i & 7, at = (i >> 3) % S::ATOMS, r = have + (i >> 3) / S::ATOMS;
+                        *reinterpret_cast<uint4*>(tile + at * KT * 128 + r * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kv_full[slot]);
+                }
+                slot = (slot + 1) % S::SLOTS;
+            } while (w.next(p, u));
+            if (!ok) abort_flag = 1;
         } else {
             constexpr uint32_t id_s = idesc_bf16(128, S::KH), id_o = idesc_bf16(128, HD) | IDESC_B_MN;
             Ring<S::SLOTS> ring;
