@@ -261,13 +261,13 @@ __global__ void __launch_bounds__(128) k_paged_simt(PagedArgs p, PagedAttnArgs a
 }
 
 // ------------------------------------------------------------------ few rows, tensor cores
-// 16 rows of one key head against groups of 16 keys that the warps take in turn, on
-// mma.m16n8k16.  What bounds it is reading the keys and values once; a tile's 16 rows are mostly
-// empty in a decode step, and the warp-level product needs no tensor memory and no barrier between
-// warps on the way.  A group lies in one page, 16 head_dim elements side by side for the keys and
-// again for the values, so each warp has them copied whole (cp.async.bulk) into a ring of its own,
-// several groups ahead; loading the fragments straight from memory left too few bytes in flight
-// beside the accumulators (64 ragged contexts, 1.1 GB: 220 us, 77 % of the copy rate).
+// 16 rows of one key head against groups of keys that the warps take in turn, on mma.m16n8k16.
+// What bounds it is reading the keys and values once; a tile's 16 rows are mostly empty in a decode
+// step, and the warp-level product needs no tensor memory and no barrier between warps on the way.
+// 16 keys lie in one page, side by side, and their values again, so each warp has them copied whole
+// (cp.async.bulk) into a ring of its own, groups ahead; loading the fragments straight from memory
+// left too few bytes in flight beside the accumulators (64 ragged contexts, 1.1 GB: 220 us, 77 % of
+// the copy rate).  Narrow heads take several 16 keys per group, which share one look at the maximum.
 //
 // The contraction over head_dim may run in any order, so lane t of a quad takes 8 consecutive
 // elements of its key (16 bytes) and the queries are loaded to match; columns of the output are
@@ -307,12 +307,14 @@ struct MmaShape {
     static constexpr int VP = HD >= 64 ? HD / 64 : 1;
     static constexpr int NT = HD / 8;                       // output tiles of 8 columns
     static constexpr int LD = HD + 4;
-    static constexpr int GROUP = 16 * HD * 2;               // bytes of a group's keys, and of its values
+    static constexpr int M = HD == 128 ? 1 : (HD == 64 ? 2 : 4);    // blocks of 16 keys in a group
+    static constexpr int BLOCK = 16 * HD * 2;               // bytes of a block's keys, and of its values
+    static constexpr int GROUP = M * 2 * BLOCK;             // [block][keys, values]
     // Stages of a warp's ring, CTAs per SM: 192 KB in flight at head widths of 128 and 64.  (At 128, two
     // CTAs with three stages take 193 us for the 64 contexts where three with two take 182 us.)
-    static constexpr int STAGES = HD == 128 ? 2 : (HD == 64 ? 3 : 4);
-    static constexpr int CTAS = HD == 128 ? 3 : (HD == 64 ? 4 : 5);
-    static constexpr int RING = MMA_WARPS * STAGES * 2 * GROUP;
+    static constexpr int STAGES = 2;
+    static constexpr int CTAS = HD >= 64 ? 3 : 4;
+    static constexpr int RING = MMA_WARPS * STAGES * GROUP;
     static constexpr int JOIN = MMA_WARPS * 16 * LD * 4;    // over the rings, when they are through
     static constexpr int SMEM = RING > JOIN ? RING : JOIN;
 };
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mm
     __syncwarp();
     pdl_wait();
     pdl_trigger();
-    uint8_t* ring = ring_sm + warp * S::STAGES * 2 * S::GROUP;
+    uint8_t* ring = ring_sm + warp * S::STAGES * S::GROUP;
     int stage = 0;                                          // of the next group to be computed
     uint32_t phase = 0;
     const float c2 = a.scale * LOG2E;
@@ -348,21 +350,27 @@ __global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mm
         const int k_begin = w.split * w.chunk, k_end = min(last + 1, k_begin + w.chunk);
         if (k_begin >= k_end) continue;
 
-        // this warp's groups: keys k_begin + 16 (warp + 4 i); lane j keeps the page of group i0 + j
-        const int n_groups = (k_end - k_begin + 15) / 16;
+        // this warp's groups: 16 M keys from k_begin + 16 M (warp + 4 i); lane j keeps the page of block
+        // b0 + j, blocks counted through the warp's groups
+        constexpr int KG = 16 * S::M;
+        const int n_groups = (k_end - k_begin + KG - 1) / KG;
         const int mine = n_groups > warp ? (n_groups - warp + MMA_WARPS - 1) / MMA_WARPS : 0;
-        auto key0 = [&](int i) { return k_begin + 16 * (warp + MMA_WARPS * i); };
+        auto key0 = [&](int i) { return k_begin + KG * (warp + MMA_WARPS * i); };
         int pages = 0, fill = stage;                        // fill: stage of the next group to be copied
         auto copy = [&](int i) {
-            if ((i & 31) == 0) pages = i + lane < mine ? max(load_page(p, w.b, key0(i + lane)), 0) : 0;
-            const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-            if (lane == 0) {
-                const bf16* src = pool + ((long long)page * 2 * p.Hkv + w.head) * head_elems +
-                                  (long long)(key0(i) & page_mask) * HD;
-                uint8_t* dst = ring + fill * 2 * S::GROUP;
-                mbar_expect_tx(&full[warp][fill], 2 * S::GROUP);
-                bulk_load(dst, src, S::GROUP, &full[warp][fill]);
-                bulk_load(dst + S::GROUP, src + v_off, S::GROUP, &full[warp][fill]);
+            if ((i * S::M & 31) == 0) {
+                const int at = key0(i + lane / S::M) + lane % S::M * 16;
+                pages = at < k_end ? max(load_page(p, w.b, at), 0) : 0;
+            }
+            const int m = lane % S::M, key = key0(i) + 16 * m;
+            const int page = __shfl_sync(0xffffffffu, pages, (i * S::M + m) & 31);
+            if (lane == 0) mbar_expect_tx(&full[warp][fill], min(S::M, (k_end - key0(i) + 15) / 16) * 2 * S::BLOCK);
+            __syncwarp();
+            if (lane < S::M && key < k_end) {
+                const bf16* src = pool + ((long long)page * 2 * p.Hkv + w.head) * head_elems + (long long)(key & page_mask) * HD;
+                uint8_t* dst = ring + fill * S::GROUP + m * 2 * S::BLOCK;
+                bulk_load(dst, src, S::BLOCK, &full[warp][fill]);
+                bulk_load(dst + S::BLOCK, src + v_off, S::BLOCK, &full[warp][fill]);
             }
             if (++fill == S::STAGES) fill = 0;
         };
@@ -396,29 +404,40 @@ __global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mm
         for (int i = 0; i < mine; ++i) {
             ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][stage], phase, nullptr));
             if (!ok) break;
-            const uint8_t* kb = ring + stage * 2 * S::GROUP;
-            float s[2][4] = {};
+            const uint8_t* kb = ring + stage * S::GROUP;
+            float s[S::M][2][4];
 #pragma unroll
-            for (int c = 0; c < S::QP; ++c) {
-                uint32_t kf[2][S::QW];
+            for (int b = 0; b < S::M; ++b)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) load_words<S::QW>(kb + (8 * n + g) * HD * 2 + (c * 4 + t) * S::QW * 4, kf[n]);
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int h = 0; h < S::QW; h += 2) {
-                    const uint32_t af[4] = {q[0][c][h], q[1][c][h], q[0][c][h + 1], q[1][c][h + 1]};
+                    for (int e = 0; e < 4; ++e) s[b][n][e] = 0.f;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) mma16816(s[n], af, kf[n][h], kf[n][h + 1]);
+            for (int c = 0; c < S::QP; ++c)
+#pragma unroll
+                for (int b = 0; b < S::M; ++b) {
+                    uint32_t kf[2][S::QW];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+                        load_words<S::QW>(kb + b * 2 * S::BLOCK + (8 * n + g) * HD * 2 + (c * 4 + t) * S::QW * 4, kf[n]);
+#pragma unroll
+                    for (int h = 0; h < S::QW; h += 2) {
+                        const uint32_t af[4] = {q[0][c][h], q[1][c][h], q[0][c][h + 1], q[1][c][h + 1]};
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma16816(s[b][n], af, kf[n][h], kf[n][h + 1]);
+                    }
                 }
-            }
             const int k0 = key0(i);
             float mx[2] = {m[0], m[1]};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int b = 0; b < S::M; ++b)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (k0 + 8 * n + 2 * t + (e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
-                    mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
-                }
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (k0 + 16 * b + 8 * n + 2 * t + (e & 1) > limit[e >> 1]) s[b][n][e] = -INFINITY;
+                        mx[e >> 1] = fmaxf(mx[e >> 1], s[b][n][e]);
+                    }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
@@ -434,39 +453,44 @@ __global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mm
                     for (int j = 0; j < S::NT; ++j) { o[j][2 * r] *= al; o[j][2 * r + 1] *= al; }
                 }
             }
-            // probabilities rounded to bf16 for the product; the sum is of the rounded values, so that
-            // the result stays a weighted mean of the values
-            uint32_t pf[4];
+            const float mc[2] = {m[0] == NEG_BIG ? 0.f : m[0] * c2, m[1] == NEG_BIG ? 0.f : m[1] * c2};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int b = 0; b < S::M; ++b) {
+                // probabilities rounded to bf16 for the product; the sum is of the rounded values, so that
+                // the result stays a weighted mean of the values
+                uint32_t pf[4];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float mc = m[r] == NEG_BIG ? 0.f : m[r] * c2;
-                    __nv_bfloat162 h = __floats2bfloat162_rn(ex2_approx(fmaf(s[n][2 * r], c2, -mc)),
-                                                             ex2_approx(fmaf(s[n][2 * r + 1], c2, -mc)));
-                    const uint32_t x = *reinterpret_cast<uint32_t*>(&h);
-                    l[r] += __uint_as_float(x << 16) + __uint_as_float(x & 0xffff0000u);
-                    pf[2 * n + r] = x;
-                }
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int c = 0; c < S::VP; ++c) {
-                uint32_t vf[4][S::VW];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int j = 2 * t + (n & 1) + 8 * (n >> 1);       // keys 2t, 2t + 1, 2t + 8, 2t + 9
-                    load_words<S::VW>(kb + S::GROUP + j * HD * 2 + (c * 8 + g) * S::VW * 4, vf[n]);
-                    if (k0 + 16 > k_end) {
-                        // slots behind the last key hold anything, and 0 * NaN is NaN
-#pragma unroll
-                        for (int e = 0; e < S::VW; ++e) vf[n][e] = k0 + j < k_end ? vf[n][e] : 0u;
+                    for (int r = 0; r < 2; ++r) {
+                        __nv_bfloat162 h = __floats2bfloat162_rn(ex2_approx(fmaf(s[b][n][2 * r], c2, -mc[r])),
+                                                                 ex2_approx(fmaf(s[b][n][2 * r + 1], c2, -mc[r])));
+                        const uint32_t x = *reinterpret_cast<uint32_t*>(&h);
+                        l[r] += __uint_as_float(x << 16) + __uint_as_float(x & 0xffff0000u);
+                        pf[2 * n + r] = x;
                     }
-                }
+                const uint8_t* vb = kb + b * 2 * S::BLOCK + S::BLOCK;
+                const int kb0 = k0 + 16 * b;
 #pragma unroll
-                for (int e = 0; e < S::VW; ++e) {
-                    mma16816(o[(c * S::VW + e) * 2], pf, __byte_perm(vf[0][e], vf[1][e], 0x5410),
-                             __byte_perm(vf[2][e], vf[3][e], 0x5410));
-                    mma16816(o[(c * S::VW + e) * 2 + 1], pf, __byte_perm(vf[0][e], vf[1][e], 0x7632),
-                             __byte_perm(vf[2][e], vf[3][e], 0x7632));
+                for (int c = 0; c < S::VP; ++c) {
+                    uint32_t vf[4][S::VW];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int j = 2 * t + (n & 1) + 8 * (n >> 1);       // keys 2t, 2t + 1, 2t + 8, 2t + 9
+                        load_words<S::VW>(vb + j * HD * 2 + (c * 8 + g) * S::VW * 4, vf[n]);
+                        if (kb0 + 16 > k_end) {
+                            // slots behind the last key hold anything, and 0 * NaN is NaN
+#pragma unroll
+                            for (int e = 0; e < S::VW; ++e) vf[n][e] = kb0 + j < k_end ? vf[n][e] : 0u;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < S::VW; ++e) {
+                        mma16816(o[(c * S::VW + e) * 2], pf, __byte_perm(vf[0][e], vf[1][e], 0x5410),
+                                 __byte_perm(vf[2][e], vf[3][e], 0x5410));
+                        mma16816(o[(c * S::VW + e) * 2 + 1], pf, __byte_perm(vf[0][e], vf[1][e], 0x7632),
+                                 __byte_perm(vf[2][e], vf[3][e], 0x7632));
+                    }
                 }
             }
             __syncwarp();                                   // the stage is read
