@@ -229,13 +229,16 @@ def _need(t: torch.Tensor, what: str, dtype, device: int, shape: tuple) -> None:
         raise ValueError(f"{what}: need {dtype} {list(shape)} on cuda:{device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
-def _row_stride(t: torch.Tensor, what: str) -> int:
-    """Elements between the rows of [N, heads, head_dim], whose rows are contiguous."""
+def _rows(t: torch.Tensor, what: str, dtype, device: int, shape: tuple) -> tuple[int, int]:
+    """(address, elements between rows) of a tensor of this type and shape [N, heads, head_dim], whose
+    rows are contiguous."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        _need(t, what, dtype, device, shape)
     s0, s1, s2 = t.stride()
-    n, h, d = t.shape
-    if s2 != 1 or (h > 1 and s1 != d):
+    n, h, d = shape
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
-    return s0 if n > 1 else h * d
+    return t.data_ptr(), s0 if n > 1 else h * d
 
 
 class PagedBatch:
@@ -464,8 +467,8 @@ class RLTModel:
         if dt is not torch.float32 and dt is not self.sdtype:
             raise ValueError(f"k: need float32 or {self.sdtype}, got {dt}")
         shape = (N, batch.n_kv_heads, hd)
-        _need(k, "k", dt, dev, shape)
-        _need(v, "v", dt, dev, shape)
+        kp, ks = _rows(k, "k", dt, dev, shape)
+        vp, vs = _rows(v, "v", dt, dev, shape)
         H = qs = os = qp = op = 0
         if q is None:
             if q_out is not None:
@@ -473,14 +476,11 @@ class RLTModel:
         else:
             H = q.shape[1]
             shape = (N, H, hd)
-            _need(q, "q", dt, dev, shape)
+            qp, qs = _rows(q, "q", dt, dev, shape)
             if q_out is None:
                 q_out = torch.empty(shape, dtype=self.sdtype, device=self.device)
-            else:
-                _need(q_out, "q_out", self.sdtype, dev, shape)
-            qs, os, qp, op = _row_stride(q, "q"), _row_stride(q_out, "q_out"), q.data_ptr(), q_out.data_ptr()
-        code = lib().rlt_paged_append(self.handle, ref, pool.data_ptr(), k.data_ptr(), _row_stride(k, "k"),
-                                      v.data_ptr(), _row_stride(v, "v"), qp, qs, H, op, os,
+            op, os = _rows(q_out, "q_out", self.sdtype, dev, shape)
+        code = lib().rlt_paged_append(self.handle, ref, pool.data_ptr(), kp, ks, vp, vs, qp, qs, H, op, os,
                                       RLT_F32 if dt is torch.float32 else RLT_BF16, self._raw_stream())
         if code:
             raise RLTError(code, "rlt_paged_append")
@@ -494,16 +494,14 @@ class RLTModel:
         ref = self._paged(batch, pool)
         H, dev = q.shape[1], self._dev
         shape = (batch.N, H, self.cfg.head_dim)
-        _need(q, "q", self.sdtype, dev, shape)
+        qp, qs = _rows(q, "q", self.sdtype, dev, shape)
         if out is None:
             out = torch.empty(shape, dtype=self.sdtype, device=self.device)
-        else:
-            _need(out, "out", self.sdtype, dev, shape)
+        op, os = _rows(out, "out", self.sdtype, dev, shape)
         # the workspace is the caller's stream's: from torch's allocator, for this call alone
         nb = batch.attention_workspace_bytes(H)
         ws = torch.empty(nb, dtype=torch.uint8, device=self.device) if nb else None
-        code = lib().rlt_paged_attention(self.handle, ref, pool.data_ptr(), q.data_ptr(), _row_stride(q, "q"), H,
-                                         out.data_ptr(), _row_stride(out, "out"), scale,
+        code = lib().rlt_paged_attention(self.handle, ref, pool.data_ptr(), qp, qs, H, op, os, scale,
                                          None if ws is None else ws.data_ptr(), nb, self._raw_stream())
         if code:
             raise RLTError(code, "rlt_paged_attention")
