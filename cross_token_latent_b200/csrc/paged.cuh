@@ -110,8 +110,10 @@ __device__ __forceinline__ int warp_iscan(int v, int lane) {
 __device__ __forceinline__ bool find_unit(const PagedArgs& p, const UnitPlan& u, int index, bool cut_items, Unit& out) {
     const int lane = threadIdx.x & 31;
     long long total = 0;
+    Seq first = {0, 0, 0};              // of sequence `lane`, for the second look
     for (int b = lane; b < p.B; b += 32) {
         const Seq s = load_seq(p, b);
+        if (b == lane) first = s;
         total += (long long)seq_tiles(u, s) * s.kv;
     }
 #pragma unroll
@@ -122,8 +124,8 @@ __device__ __forceinline__ bool find_unit(const PagedArgs& p, const UnitPlan& u,
     const int chunk = c < u.min_chunk ? u.min_chunk : (c > (1 << 30) ? 1 << 30 : (int)c);
     int base = 0, slot_base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        Seq s = {0, 0, 0};
-        if (b0 + lane < p.B) s = load_seq(p, b0 + lane);
+        Seq s = first;
+        if (b0 > 0) s = b0 + lane < p.B ? load_seq(p, b0 + lane) : Seq{0, 0, 0};
         const int tiles = seq_tiles(u, s) * p.Hkv;
         const int ns = s.kv > chunk ? (s.kv + chunk - 1) / chunk : 1;
         const int slots = ns > 1 ? tiles * ns : 0;

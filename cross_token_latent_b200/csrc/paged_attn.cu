@@ -123,143 +123,6 @@ __global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a
     for (int k = 0; k < JOIN_COLS; k += Vec16<T>::N) st16(o + k, Vec16<T>::pack(acc + k));
 }
 
-// ------------------------------------------------------------------ CUDA cores
-// 2 R rows of one key head against tiles of 64 keys in shared memory; thread t scores key t % 64
-// for R rows, then owns a column of the output for some of the rows.  Float32 throughout.
-template <typename T, int HD, int R>
-__global__ void __launch_bounds__(128) k_paged_simt(PagedArgs p, PagedAttnArgs a, UnitPlan u) {
-    constexpr int RT = 2 * R, KT = 64, LD = HD + 4;
-    constexpr int GROUPS = 128 / HD, RPG = RT >= GROUPS ? RT / GROUPS : 1;      // rows per column group
-    extern __shared__ __align__(16) float sm[];
-    float* Ks = sm;                     // [KT][LD]
-    float* Vs = Ks + KT * LD;           // [KT][HD]
-    float* Qs = Vs + KT * HD;           // [RT][HD]
-    float* Ps = Qs + RT * HD;           // [RT][KT]
-    float* Al = Ps + RT * KT;           // [RT] rescale of the accumulators, then the sums
-    pdl_wait();
-    pdl_trigger();
-    Unit w;
-    if (!find_unit(p, u, blockIdx.x, false, w)) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rows = min(RT, w.s.nq * u.g - w.tile * RT);
-    const int row0 = w.tile * RT, ctx = w.s.kv - w.s.nq;
-    const int last = ctx + (row0 + rows - 1) / u.g;                 // the last key any row sees
-    const int k_begin = w.split * w.chunk, k_end = min(last + 1, k_begin + w.chunk);
-    if (k_begin >= k_end) return;                                   // this tile ends in front of the unit
-    for (int i = tid; i < RT * HD; i += 128) {
-        const int r = i / HD, row = row0 + r;
-        float x = 0.f;
-        if (r < rows)
-            x = to_f(reinterpret_cast<const T*>(a.q)[(w.s.q0 + row / u.g) * a.q_stride +
-                                                     (long long)(w.head * u.g + row % u.g) * HD + i % HD]);
-        Qs[i] = x * (a.scale * LOG2E);
-    }
-    float m[RT / 4 > 0 ? RT / 4 : 1], l[RT / 4 > 0 ? RT / 4 : 1];   // of the rows this warp keeps
-#pragma unroll
-    for (int i = 0; i < (RT / 4 > 0 ? RT / 4 : 1); ++i) { m[i] = NEG_BIG; l[i] = 0.f; }
-    float acc[RPG];
-#pragma unroll
-    for (int i = 0; i < RPG; ++i) acc[i] = 0.f;
-    const int col = tid % HD, grp = tid / HD;
-    constexpr int E = Vec16<T>::N, PIECES = HD / E;                 // 16-byte pieces of a key
-    const T* pool = reinterpret_cast<const T*>(a.pool);
-    const long long head_elems = (long long)HD << p.page_shift;
-    for (int k0 = k_begin; k0 < k_end; k0 += KT) {
-        __syncthreads();
-        for (int i = tid; i < KT * PIECES; i += 128) {
-            const int j = i / PIECES, c = (i % PIECES) * E, key = k0 + j;
-            float kx[E], vx[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) kx[e] = vx[e] = 0.f;
-            if (key < k_end) {
-                const int page = max(load_page(p, w.b, key), 0);
-                const long long at = ((long long)page * 2 * p.Hkv + w.head) * head_elems +
-                                     (long long)(key & ((1 << p.page_shift) - 1)) * HD + c;
-                Vec16<T>::unpack(ld16(pool + at), kx);
-                Vec16<T>::unpack(ld16(pool + at + p.Hkv * head_elems), vx);
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) { Ks[j * LD + c + e] = kx[e]; Vs[j * HD + c + e] = vx[e]; }
-        }
-        __syncthreads();
-        {
-            const int j = tid & 63, half = tid >> 6, key = k0 + j;
-            float s[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) s[r] = 0.f;
-            for (int c = 0; c < HD; c += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(&Ks[j * LD + c]);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float4 q4 = *reinterpret_cast<const float4*>(&Qs[(half * R + r) * HD + c]);
-                    s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int row = half * R + r;
-                const bool seen = row < rows && key < k_end && key <= ctx + (row0 + row) / u.g;
-                Ps[row * KT + j] = seen ? s[r] : -INFINITY;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < (RT / 4 > 0 ? RT / 4 : 1); ++i) {
-            const int r = warp + 4 * i;
-            if (r < RT) {
-                const float s0 = Ps[r * KT + lane], s1 = Ps[r * KT + lane + 32];
-                const float mx = fmaxf(m[i], warp_max(fmaxf(s0, s1)));
-                const float p0 = exp2f(s0 - mx), p1 = exp2f(s1 - mx), al = exp2f(m[i] - mx);
-                l[i] = l[i] * al + warp_sum(p0 + p1);
-                m[i] = mx;
-                Ps[r * KT + lane] = p0;
-                Ps[r * KT + lane + 32] = p1;
-                if (lane == 0) Al[r] = al;
-            }
-        }
-        __syncthreads();
-        if (grp * RPG < RT) {
-#pragma unroll
-            for (int i = 0; i < RPG; ++i) acc[i] *= Al[grp * RPG + i];
-            for (int j = 0; j < KT; j += 4) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = Vs[(j + e) * HD + col];
-#pragma unroll
-                for (int i = 0; i < RPG; ++i) {
-                    const float4 p4 = *reinterpret_cast<const float4*>(&Ps[(grp * RPG + i) * KT + j]);
-                    acc[i] = fmaf(p4.x, v[0], fmaf(p4.y, v[1], fmaf(p4.z, v[2], fmaf(p4.w, v[3], acc[i]))));
-                }
-            }
-        }
-    }
-    __syncthreads();
-    float* Mx = Ps;                     // the rows' maxima, beside their sums
-#pragma unroll
-    for (int i = 0; i < (RT / 4 > 0 ? RT / 4 : 1); ++i) {
-        const int r = warp + 4 * i;
-        if (r < RT && lane == 0) { Al[r] = l[i]; Mx[r] = m[i]; }
-    }
-    __syncthreads();
-    if (grp * RPG < RT) {
-#pragma unroll
-        for (int i = 0; i < RPG; ++i) {
-            const int r = grp * RPG + i, row = row0 + r;
-            if (r < rows) {
-                if (w.n_splits > 1) {
-                    float* pr = part_row(a, u, w.slot, r, HD);
-                    pr[col] = acc[i];
-                    if (col == 0) { pr[HD] = Mx[r]; pr[HD + 1] = Al[r]; }
-                } else {
-                    reinterpret_cast<T*>(a.o)[(w.s.q0 + row / u.g) * a.o_stride +
-                                              (long long)(w.head * u.g + row % u.g) * HD + col] =
-                        from_f<T>(acc[i] / Al[r]);
-                }
-            }
-        }
-    }
-}
-
 // ------------------------------------------------------------------ few rows, tensor cores
 // 16 rows of one key head against groups of keys that the warps take in turn, on mma.m16n8k16.
 // What bounds it is reading the keys and values once; a tile's 16 rows are mostly empty in a decode
@@ -560,24 +423,209 @@ __global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mm
     }
 }
 
-UnitPlan make_plan(const PagedArgs& p, int H, int rt, int rows_lo, int rows_hi, int min_chunk, int align, int target) {
+// ------------------------------------------------------------------ float32
+// 8 rows of one key head against groups of 16 keys, every warp on its own as above, on the CUDA cores
+// in float32 throughout (the tensor cores' formats would not hold the float32 model's results).  Lane
+// 16 j + k scores key k for rows 4 j .. 4 j + 3 and then has columns k, k + 16, .. of the output of
+// those rows, the probabilities going round by shared memory.  Scoring, the four elements of a key that a
+// lane takes next are the (step + key)-th: side by side, keys lie HD floats apart, and lanes that all
+// took the same would meet in the same banks.  What bounds it is the products themselves, and in a
+// decode step the reading of the keys and values.
+template <int HD>
+struct F32Shape {
+    static constexpr int RT = 8;
+    static constexpr int LD = HD + 4;
+    static constexpr int BLOCK = 16 * HD * 4;               // bytes of a group's keys, and of its values
+    static constexpr int STAGES = 2;
+    static constexpr int CTAS = HD == 128 ? 1 : (HD == 64 ? 3 : 5);
+    static constexpr int RING = MMA_WARPS * STAGES * 2 * BLOCK;
+    static constexpr int JOIN = MMA_WARPS * RT * LD * 4;    // over the rings, when they are through
+    static constexpr int ROWS = RT * HD * 4;                // the queries, behind them
+    static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + ROWS;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(MMA_WARPS * 32, F32Shape<HD>::CTAS) k_paged_f32(PagedArgs p, PagedAttnArgs a, UnitPlan u) {
+    using S = F32Shape<HD>;
+    constexpr int NC = HD / 16, NP = HD / 4;                // columns per lane, 16-byte pieces of a key
+    extern __shared__ __align__(128) uint8_t ring_sm[];     // [warps][STAGES][keys, values]
+    float* sm = reinterpret_cast<float*>(ring_sm);          // [warps][RT][LD]: accumulators, maximum, sum
+    float* qs = reinterpret_cast<float*>(ring_sm + S::SMEM - S::ROWS);
+    __shared__ __align__(16) float ps[MMA_WARPS][S::RT][16];        // probabilities of a warp's group
+    __shared__ uint64_t full[MMA_WARPS][S::STAGES];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = lane >> 4, k = lane & 15;
+    if (lane == 0) {
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(&full[warp][i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    pdl_wait();
+    pdl_trigger();
+    Unit w;
+    if (!find_unit(p, u, blockIdx.x, false, w)) return;
+    const int row0 = w.tile * S::RT, rows = min(S::RT, w.s.nq * u.g - row0), ctx = w.s.kv - w.s.nq;
+    const int last = ctx + (row0 + rows - 1) / u.g;
+    const int k_begin = w.split * w.chunk, k_end = min(last + 1, k_begin + w.chunk);
+    if (k_begin >= k_end) return;
+
+    uint8_t* ring = ring_sm + warp * S::STAGES * 2 * S::BLOCK;
+    const float* pool = reinterpret_cast<const float*>(a.pool);
+    const long long head_elems = (long long)HD << p.page_shift, v_off = p.Hkv * head_elems;
+    const int n_groups = (k_end - k_begin + 15) / 16;
+    const int mine = n_groups > warp ? (n_groups - warp + MMA_WARPS - 1) / MMA_WARPS : 0;
+    auto key0 = [&](int i) { return k_begin + 16 * (warp + MMA_WARPS * i); };
+    int pages = 0;
+    auto copy = [&](int i) {
+        if ((i & 31) == 0) pages = i + lane < mine ? max(load_page(p, w.b, key0(i + lane)), 0) : 0;
+        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+        if (lane == 0) {
+            const float* src = pool + ((long long)page * 2 * p.Hkv + w.head) * head_elems +
+                               (long long)(key0(i) & ((1 << p.page_shift) - 1)) * HD;
+            uint8_t* dst = ring + i % S::STAGES * 2 * S::BLOCK;
+            uint64_t* bar = &full[warp][i % S::STAGES];
+            mbar_expect_tx(bar, 2 * S::BLOCK);
+            bulk_load(dst, src, S::BLOCK, bar);
+            bulk_load(dst + S::BLOCK, src + v_off, S::BLOCK, bar);
+        }
+    };
+    for (int i = 0; i < S::STAGES && i < mine; ++i) copy(i);
+    for (int i = threadIdx.x; i < S::RT * HD; i += MMA_WARPS * 32) {
+        const int r = i / HD, row = row0 + r;
+        float x = 0.f;
+        if (r < rows)
+            x = reinterpret_cast<const float*>(a.q)[(w.s.q0 + row / u.g) * a.q_stride +
+                                                    (long long)(w.head * u.g + row % u.g) * HD + i % HD];
+        qs[i] = x * (a.scale * LOG2E);
+    }
+    __syncthreads();
+
+    float m[4], l[4], o[4][NC];                             // l: of this lane's keys
+    int limit[4];                                           // the last key of rows 4 half + r
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = 4 * half + r;
+        limit[r] = i < rows ? ctx + (row0 + i) / u.g : -1;
+        m[r] = NEG_BIG;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[r][c] = 0.f;
+    }
+    bool ok = true;
+    int done = 0;
+    for (; done < mine; ++done) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][done % S::STAGES], done / S::STAGES & 1, nullptr));
+        if (!ok) break;
+        const float* kb = reinterpret_cast<const float*>(ring + done % S::STAGES * 2 * S::BLOCK);
+        const float* vb = kb + 16 * HD;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int c = 0; c < NP; ++c) {
+            const int at = (c + k) % NP * 4;
+            const float4 x = *reinterpret_cast<const float4*>(kb + k * HD + at);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 q = *reinterpret_cast<const float4*>(qs + (4 * half + r) * HD + at);
+                s[r] = fmaf(q.x, x.x, fmaf(q.y, x.y, fmaf(q.z, x.z, fmaf(q.w, x.w, s[r]))));
+            }
+        }
+        const int key = key0(done) + k;
+        float mx[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (key > limit[r] || key >= k_end) s[r] = -INFINITY;
+            mx[r] = fmaxf(m[r], s[r]);
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], d));
+            const float al = ex2_approx(m[r] - mx[r]);
+            m[r] = mx[r];
+            s[r] = ex2_approx(s[r] - mx[r]);
+            l[r] = l[r] * al + s[r];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[r][c] *= al;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ps[warp][4 * half + r][k] = s[r];
+        __syncwarp();
+        const int have = k_end - key0(done);                // (values behind the last key hold anything)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            float4 pr[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pr[r] = *reinterpret_cast<const float4*>(&ps[warp][4 * half + r][j]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = j + e < have ? vb[(j + e) * HD + 16 * c + k] : 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    o[r][c] = fmaf(pr[r].x, v[0], fmaf(pr[r].y, v[1], fmaf(pr[r].z, v[2], fmaf(pr[r].w, v[3], o[r][c]))));
+            }
+        }
+        __syncwarp();                                       // the stage is read
+        if (done + S::STAGES < mine) copy(done + S::STAGES);
+    }
+    if (!ok && lane == 0) {
+        raise_flag(p.hdr, ERR_TIMEOUT);
+        // the copies in flight land before the shared memory is given back
+        for (int i = done; i < mine && i < done + S::STAGES; ++i)
+            mbar_wait(&full[warp][i % S::STAGES], i / S::STAGES & 1, nullptr);
+    }
+    if (__syncthreads_or(!ok)) return;                      // (behind it the rings are through)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
+        float* dst = sm + (warp * S::RT + 4 * half + r) * S::LD;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) dst[16 * c + k] = o[r][c];
+        if (k == 0) { dst[HD] = m[r]; dst[HD + 1] = l[r]; }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * HD; i += MMA_WARPS * 32) {
+        const int r = i / HD, col = i % HD;
+        float mt = NEG_BIG;
+#pragma unroll
+        for (int x = 0; x < MMA_WARPS; ++x) mt = fmaxf(mt, sm[(x * S::RT + r) * S::LD + HD]);
+        float lt = 0.f, acc = 0.f;
+#pragma unroll
+        for (int x = 0; x < MMA_WARPS; ++x) {
+            const float* src = sm + (x * S::RT + r) * S::LD;
+            const float f = ex2_approx(src[HD] - mt);
+            lt += f * src[HD + 1];
+            acc += f * src[col];
+        }
+        if (w.n_splits > 1) {
+            float* pr = part_row(a, u, w.slot, r, HD);
+            pr[col] = acc;
+            if (col == 0) { pr[HD] = mt; pr[HD + 1] = lt; }
+        } else {
+            const int row = row0 + r;
+            reinterpret_cast<float*>(a.o)[(long long)(w.s.q0 + row / u.g) * a.o_stride +
+                                          (long long)(w.head * u.g + row % u.g) * HD + col] = acc / lt;
+        }
+    }
+}
+
+// About nine units per SM, and none shorter than 256 keys; where there are items enough to go round
+// (128 at a head width of 128, 64 at 64), none shorter than 1024, because joining costs a launch and the
+// cut items' states.  (Contexts up to 1000, 8 key heads of 128: one sequence takes 12.6 us with pieces of
+// 256 and 17.4 whole, 256 sequences take 139 us and 118.)
+UnitPlan make_plan(const PagedArgs& p, int H, int hd, int rt, int rows_lo, int rows_hi) {
     UnitPlan u;
     u.g = H / p.Hkv;
     u.rt = rt;
     u.rows_lo = rows_lo;
     u.rows_hi = rows_hi;
-    u.min_chunk = min_chunk;
-    u.chunk_align = align;
-    u.target = target;
+    u.min_chunk = plan_items(p, u) >= hd ? 1024 : 256;
+    u.chunk_align = 64;
+    u.target = 148 * 9;
     u.slots = (int)plan_slots(p, u);
     u.part = 0;
     return u;
 }
 constexpr int ANY = 1 << 30;
-// Float32: 2 rows per unit when no sequence has more, else 16.
-UnitPlan simt_plan(const PagedArgs& p, int H) {
-    return make_plan(p, H, (long long)p.max_q * (H / p.Hkv) <= 2 ? 2 : 16, 1, ANY, 256, 64, 148 * 8);
-}
+UnitPlan f32_plan(const PagedArgs& p, int H, int hd) { return make_plan(p, H, hd, 8, 1, ANY); }
 
 // bf16: sequences of at most FEW_ROWS rows per key head go to the warp-level kernel, those of more
 // to the tcgen05 kernel, which head widths of 64 and 128 have (and pools whose rows TMA can count).
@@ -595,7 +643,7 @@ Bf16Plans bf16_plans(const PagedArgs& p, int H, int hd) {
            (((long long)p.n_pages * 2 * p.Hkv) << p.page_shift) < (1LL << 31);
     PagedArgs few = p;              // its bounds
     if (b.tc) few.max_q = FEW_ROWS / g < 1 ? 1 : FEW_ROWS / g;
-    b.u_mma = make_plan(few, H, 16, 1, b.tc ? FEW_ROWS : ANY, 256, 64, 148 * 9);
+    b.u_mma = make_plan(few, H, hd, 16, 1, b.tc ? FEW_ROWS : ANY);
     b.floats = (size_t)b.u_mma.slots * b.u_mma.rt * (hd + 2);
     b.u_tc = {};
     if (b.tc) {
@@ -629,24 +677,12 @@ cudaError_t run_mma(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const 
     return launch_k(L, k_paged_mma<HD>, (unsigned)grid, MMA_WARPS * 32, MmaShape<HD>::SMEM, p, a, u, units);
 }
 
-template <typename T, int HD, int R>
-cudaError_t run_simt(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
-    constexpr int RT = 2 * R;
-    constexpr size_t smem = (64 * (HD + 4) + 64 * HD + RT * HD + RT * 64 + RT) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(k_paged_simt<T, HD, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <int HD>
+cudaError_t run_f32(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
+    cudaError_t e = cudaFuncSetAttribute(k_paged_f32<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32Shape<HD>::SMEM);
     if (e != cudaSuccess) return e;
     const long long grid = plan_items(p, u) + (u.slots ? u.target : 0);
-    return launch_k(L, k_paged_simt<T, HD, R>, (unsigned)grid, 128, smem, p, a, u);
-}
-template <typename T, int R>
-cudaError_t run_simt_hd(Launch L, const PagedArgs& p, const PagedAttnArgs& a, const UnitPlan& u) {
-    switch (a.hd) {
-        case 16: return run_simt<T, 16, R>(L, p, a, u);
-        case 32: return run_simt<T, 32, R>(L, p, a, u);
-        case 64: return run_simt<T, 64, R>(L, p, a, u);
-        case 128: return run_simt<T, 128, R>(L, p, a, u);
-    }
-    return cudaErrorInvalidValue;
+    return launch_k(L, k_paged_f32<HD>, (unsigned)grid, MMA_WARPS * 32, F32Shape<HD>::SMEM, p, a, u);
 }
 
 // At most one cut item per two slots, `target` of them, and no more than there are items.
@@ -659,7 +695,7 @@ int join_items(const UnitPlan& u, long long items) {
 
 size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16) {
     if (!is_bf16) {
-        const UnitPlan u = simt_plan(p, H);
+        const UnitPlan u = f32_plan(p, H, hd);
         return (size_t)u.slots * u.rt * (hd + 2) * sizeof(float);
     }
     return bf16_plans(p, H, hd).floats * sizeof(float);
@@ -667,8 +703,14 @@ size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16) {
 
 template <>
 cudaError_t launch_paged_attention<float>(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
-    const UnitPlan u = simt_plan(p, a.H);
-    cudaError_t e = u.rt == 2 ? run_simt_hd<float, 1>(L, p, a, u) : run_simt_hd<float, 8>(L, p, a, u);
+    const UnitPlan u = f32_plan(p, a.H, a.hd);
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (a.hd) {
+        case 16: e = run_f32<16>(L, p, a, u); break;
+        case 32: e = run_f32<32>(L, p, a, u); break;
+        case 64: e = run_f32<64>(L, p, a, u); break;
+        case 128: e = run_f32<128>(L, p, a, u); break;
+    }
     const int n = join_items(u, plan_items(p, u));
     if (e != cudaSuccess || n == 0) return e;
     return launch_k(L, k_paged_join<float>, dim3(n), 128, 0, p, a, u, n, SharePlan{});
