@@ -14,76 +14,74 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NEG_BIG = -1e30f;
 
-// Rows i0, i0 + stride, .. (JOIN_WARP_ROWS of them, those below `rows`) of a cut item, by a warp: row i
-// is joined from n(i) partial states, state j of it at r(j, i), into o(i).  The rows' loads are in flight
-// together.
-constexpr int JOIN_WARP_ROWS = 4;
-template <typename T, typename N, typename R, typename O>
-__device__ __forceinline__ void join_rows(int i0, int stride, int rows, int hd, N n, R r, O o) {
-    const int lane = threadIdx.x & 31;
-    constexpr int K = JOIN_WARP_ROWS;
-    float m[K], l[K], acc[K][4];
-    int cnt[K], most = 0;
+// One output row of a cut item from n partial states, by a block of 128 threads; state j's row is at
+// states + j * stride.  128 states at a time: a thread per state looks at its maximum and sum, then threads over the
+// columns (and over the states, where a row has fewer columns than there are threads) add them up.
+constexpr int JOIN_THREADS = 128;
+template <typename T>
+__device__ __forceinline__ void join_row(T* o, int hd, int n, const float* __restrict__ states, long long stride) {
+    __shared__ float weight[JOIN_THREADS], top[4], sums[4], acc_sm[JOIN_THREADS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int col = tid % hd, part = tid / hd, parts = JOIN_THREADS / hd;
+    float m = NEG_BIG, l = 0.f, acc = 0.f;
+    for (int j0 = 0; j0 < n; j0 += JOIN_THREADS) {
+        const int here = min(JOIN_THREADS, n - j0);
+        float2 ml = make_float2(NEG_BIG, 0.f);
+        const float* now = states + j0 * stride;
+        if (tid < here) ml = *reinterpret_cast<const float2*>(now + tid * stride + hd);
+        const float mw = warp_max(ml.x);
+        if (lane == 0) top[warp] = mw;
+        __syncthreads();
+        const float to = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+        const float w = exp2f(ml.x - to), old = exp2f(m - to);
+        weight[tid] = w;
+        const float lw = warp_sum(w * ml.y);
+        if (lane == 0) sums[warp] = lw;
+        __syncthreads();
+        l = l * old + ((sums[0] + sums[1]) + (sums[2] + sums[3]));
+        acc *= old;
+        m = to;
+        for (int j = part; j < here; j += 8 * parts) {
+            float v[8];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int i = i0 + k * stride;
-        cnt[k] = i < rows ? n(i) : 0;
-        most = max(most, cnt[k]);
-        m[k] = NEG_BIG;
-        l[k] = 0.f;
+            for (int k = 0; k < 8; ++k) v[k] = j + k * parts < here ? now[(j + k * parts) * stride + col] : 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[k][c] = 0.f;
-    }
-    for (int j = 0; j < most; ++j) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (j >= cnt[k]) continue;
-            const float* x = r(j, i0 + k * stride);
-            const float2 ml = *reinterpret_cast<const float2*>(x + hd);
-            const float to = fmaxf(m[k], ml.x), f0 = exp2f(m[k] - to), f1 = exp2f(ml.x - to);
-            m[k] = to;
-            l[k] = l[k] * f0 + ml.y * f1;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c * 32 + lane < hd) acc[k][c] = acc[k][c] * f0 + x[c * 32 + lane] * f1;
+            for (int k = 0; k < 8; ++k) acc = fmaf(j + k * parts < here ? weight[j + k * parts] : 0.f, v[k], acc);
         }
+        __syncthreads();                        // the weights are read
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        if (cnt[k] == 0) continue;
-        T* out = o(i0 + k * stride);
-        const float inv = 1.0f / l[k];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (c * 32 + lane < hd) out[c * 32 + lane] = from_f<T>(acc[k][c] * inv);
+    acc_sm[tid] = acc;
+    __syncthreads();
+    if (part == 0) {
+        for (int i = 1; i < parts; ++i) acc += acc_sm[i * hd + col];
+        o[col] = from_f<T>(acc / l);
     }
 }
 
-// Joins the partial states of the cut items.  The first n1 blocks of x are cut items of the plan u (16
-// rows and fewer).  With the plan us, block n1 + c - 1 is the item that share c begins inside of, if
-// share c is the first to: 128 rows, a thread each, of 32 columns (y: column and row blocks).
-constexpr int JOIN_COLS = 32;
+// Joins the partial states of the cut items.  The first n1 blocks of x are cut items of the plan u, whose
+// rows the first y1 blocks of y take in turn.  With the plan us, block n1 + c - 1 is the item that share c begins inside of, if share c is the
+// first to: 128 rows, a thread each, of 8 columns (y: column and row blocks).
+constexpr int JOIN_COLS = 8;
 template <typename T>
-__global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u, int n1, SharePlan us) {
+__global__ void __launch_bounds__(JOIN_THREADS) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u, int n1,
+                                                             int y1, SharePlan us) {
     if ((int)blockIdx.x < n1) {
         // The kernel in front waited for its predecessor before it let this one start, so the batch's
         // lengths may be read here; the partial states only behind the wait.
         Unit w;
-        const bool any = blockIdx.y == 0 && find_unit(p, u, blockIdx.x, true, w);
+        const bool any = (int)blockIdx.y < y1 && find_unit(p, u, blockIdx.x, true, w);
         pdl_wait();
         pdl_trigger();
         if (!any) return;
-        const int row0 = w.tile * u.rt, ctx = w.s.kv - w.s.nq;
-        join_rows<T>(
-            threadIdx.x >> 5, 4, min(u.rt, w.s.nq * u.g - row0), a.hd,
-            [&](int i) {                        // units that saw a key of this row
-                return min(w.n_splits, (ctx + (row0 + i) / u.g + 1 + w.chunk - 1) / w.chunk);
-            },
-            [&](int j, int i) { return part_row(a, u, w.slot + j, i, a.hd); },
-            [&](int i) {
-                return reinterpret_cast<T*>(a.o) + (w.s.q0 + (row0 + i) / u.g) * a.o_stride +
-                       (long long)(w.head * u.g + (row0 + i) % u.g) * a.hd;
-            });
+        const int row0 = w.tile * u.rt, rows = min(u.rt, w.s.nq * u.g - row0);
+        for (int i = blockIdx.y; i < rows; i += y1) {
+            const int tok = (row0 + i) / u.g, keys = w.s.kv - w.s.nq + tok + 1;
+            const int n = min(w.n_splits, (keys + w.chunk - 1) / w.chunk);      // units that saw a key of this row
+            T* o = reinterpret_cast<T*>(a.o) + (w.s.q0 + tok) * a.o_stride +
+                   (long long)(w.head * u.g + (row0 + i) % u.g) * a.hd;
+            join_row(o, a.hd, n, part_row(a, u, w.slot, i, a.hd), (long long)u.rt * (a.hd + 2));
+            __syncthreads();                    // its shared memory is free
+        }
         return;
     }
     pdl_wait();
@@ -92,7 +90,7 @@ __global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a
     const ShareCut cut = reinterpret_cast<const ShareCut*>(a.part + us.cuts)[c];
     if (cut.step == 0) return;
     const int c0 = (int)(cut.begin / cut.share), row0 = cut.tile * us.rt;
-    const int cols = a.hd / JOIN_COLS, i = blockIdx.y / cols * 128 + threadIdx.x, col = blockIdx.y % cols * JOIN_COLS;
+    const int cols = a.hd / JOIN_COLS, i = blockIdx.y / cols * JOIN_THREADS + threadIdx.x, col = blockIdx.y % cols * JOIN_COLS;
     if (c0 != c - 1 || i >= us.rt || row0 + i >= cut.s.nq * us.g) return;
     const int tok = (row0 + i) / us.g;
     // shares up to the step of the row's last key
@@ -102,17 +100,33 @@ __global__ void __launch_bounds__(128) k_paged_join(PagedArgs p, PagedAttnArgs a
     float m = NEG_BIG, l = 0.f, acc[JOIN_COLS];
 #pragma unroll
     for (int k = 0; k < JOIN_COLS; ++k) acc[k] = 0.f;
-    for (int j = 0; j < n; ++j) {
-        const float* x = share_part(a, us, j == 0 ? first : 2 * (c0 + j), a.hd) + i;
-        float v[JOIN_COLS];
+    constexpr int AHEAD = 4;                    // states whose loads are in flight together
+    for (int j0 = 0; j0 < n; j0 += AHEAD) {
+        float v[AHEAD][JOIN_COLS], mj[AHEAD], lj[AHEAD];
+        float to = m;
 #pragma unroll
-        for (int k = 0; k < JOIN_COLS; ++k) v[k] = x[(col + k) * us.rt];
-        const float mj = x[a.hd * us.rt], lj = x[(a.hd + 1) * us.rt];
-        const float to = fmaxf(m, mj), f0 = exp2f(m - to), f1 = exp2f(mj - to);
+        for (int b = 0; b < AHEAD; ++b) {
+            const int j = min(j0 + b, n - 1);
+            const float* x = share_part(a, us, j == 0 ? first : 2 * (c0 + j), a.hd) + i;
+#pragma unroll
+            for (int k = 0; k < JOIN_COLS; ++k) v[b][k] = x[(col + k) * us.rt];
+            mj[b] = j0 + b < n ? x[a.hd * us.rt] : NEG_BIG;
+            lj[b] = x[(a.hd + 1) * us.rt];
+        }
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) to = fmaxf(to, mj[b]);
+        const float old = exp2f(m - to);
         m = to;
-        l = l * f0 + lj * f1;
+        l *= old;
 #pragma unroll
-        for (int k = 0; k < JOIN_COLS; ++k) acc[k] = acc[k] * f0 + v[k] * f1;
+        for (int k = 0; k < JOIN_COLS; ++k) acc[k] *= old;
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) {
+            const float f = exp2f(mj[b] - to);
+            l = fmaf(lj[b], f, l);
+#pragma unroll
+            for (int k = 0; k < JOIN_COLS; ++k) acc[k] = fmaf(v[b][k], f, acc[k]);
+        }
     }
     const float inv = 1.0f / l;
     T* o = reinterpret_cast<T*>(a.o) + (cut.s.q0 + tok) * a.o_stride +
@@ -691,6 +705,14 @@ int join_items(const UnitPlan& u, long long items) {
     return u.slots == 0 ? 0 : (int)n;
 }
 
+// Blocks that share the rows of a cut item: as many as a tile can have rows, while the items alone do
+// not fill the GPU.
+int join_rows(const PagedArgs& p, const UnitPlan& u, int items) {
+    const long long rows = (long long)p.max_q * u.g;
+    const int most = rows < u.rt ? (int)rows : u.rt, want = (sm_count() * 8 + items - 1) / items;
+    return want < most ? want : most;
+}
+
 }  // namespace
 
 size_t paged_attn_workspace(const PagedArgs& p, int H, int hd, bool is_bf16) {
@@ -713,7 +735,8 @@ cudaError_t launch_paged_attention<float>(Launch L, const PagedArgs& p, const Pa
     }
     const int n = join_items(u, plan_items(p, u));
     if (e != cudaSuccess || n == 0) return e;
-    return launch_k(L, k_paged_join<float>, dim3(n), 128, 0, p, a, u, n, SharePlan{});
+    const int y = join_rows(p, u, n);
+    return launch_k(L, k_paged_join<float>, dim3(n, y), JOIN_THREADS, 0, p, a, u, n, y, SharePlan{});
 }
 template <>
 cudaError_t launch_paged_attention<bf16>(Launch L, const PagedArgs& p, const PagedAttnArgs& a) {
@@ -731,8 +754,10 @@ cudaError_t launch_paged_attention<bf16>(Launch L, const PagedArgs& p, const Pag
     if (e != cudaSuccess) return e;
     const int n1 = join_items(b.u_mma, mma_items), n2 = b.tc && !b.u_tc.whole ? b.u_tc.ctas - 1 : 0;
     if (n1 + n2 == 0) return e;
-    const int y = n2 ? (b.u_tc.rt + 127) / 128 * (a.hd / JOIN_COLS) : 1;
-    return launch_k(L, k_paged_join<bf16>, dim3(n1 + n2, y), 128, 0, p, a, b.u_mma, n1, b.u_tc);
+    const int y1 = n1 ? join_rows(p, b.u_mma, n1) : 1;
+    const int y2 = n2 ? (b.u_tc.rt + JOIN_THREADS - 1) / JOIN_THREADS * (a.hd / JOIN_COLS) : 1;
+    return launch_k(L, k_paged_join<bf16>, dim3(n1 + n2, y1 > y2 ? y1 : y2), JOIN_THREADS, 0, p, a, b.u_mma, n1, y1,
+                    b.u_tc);
 }
 
 }  // namespace rlt
