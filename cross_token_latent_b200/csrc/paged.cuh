@@ -141,6 +141,7 @@ __device__ __forceinline__ bool find_unit(const PagedArgs& p, const UnitPlan& u,
             out.n_splits = __shfl_sync(0xffffffffu, ns, src);
             out.chunk = chunk;
             int i = index - __shfl_sync(0xffffffffu, end - mine, src);
+            const bool counted = i >= 0;
             const int slot0 = __shfl_sync(0xffffffffu, slot_end - slots, src);
             // the last tiles of a sequence see the most keys: they start first
             if (cut_items) {
@@ -153,8 +154,8 @@ __device__ __forceinline__ bool find_unit(const PagedArgs& p, const UnitPlan& u,
             out.tile = seq_tiles(u, out.s) - 1 - i / p.Hkv;
             out.slot = slot0 + i * out.n_splits + out.split;
             // Starts that overlap count rows twice, so that there are more units than the host sized
-            // for: those beyond are left out.
-            if (out.tile >= 0 && out.slot >= 0 && (out.n_splits == 1 || out.slot < u.slots)) return true;
+            // for, even more than an int counts: those beyond are left out.
+            if (counted && out.tile >= 0 && (out.n_splits == 1 || (out.slot >= 0 && out.slot < u.slots))) return true;
             raise_flag(p.hdr, ERR_BAD_PAGE);
             return false;
         }

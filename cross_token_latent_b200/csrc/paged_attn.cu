@@ -15,8 +15,9 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NEG_BIG = -1e30f;
 
 // One output row of a cut item from n partial states, by a block of 128 threads; state j's row is at
-// states + j * stride.  128 states at a time: a thread per state looks at its maximum and sum, then threads over the
-// columns (and over the states, where a row has fewer columns than there are threads) add them up.
+// states + j * stride.  128 states at a time: a thread per state looks at its maximum and sum, then
+// threads over the columns (and over the states, where a row has fewer columns than there are
+// threads) add them up.
 constexpr int JOIN_THREADS = 128;
 template <typename T>
 __device__ __forceinline__ void join_row(T* o, int hd, int n, const float* __restrict__ states, long long stride) {
@@ -58,9 +59,10 @@ __device__ __forceinline__ void join_row(T* o, int hd, int n, const float* __res
     }
 }
 
-// Joins the partial states of the cut items.  The first n1 blocks of x are cut items of the plan u, whose
-// rows the first y1 blocks of y take in turn.  With the plan us, block n1 + c - 1 is the item that share c begins inside of, if share c is the
-// first to: 128 rows, a thread each, of 8 columns (y: column and row blocks).
+// Joins the partial states of the cut items.  The first n1 blocks of x are cut items of the plan u,
+// whose rows the first y1 blocks of y take in turn.  With the plan us, block n1 + c - 1 is the item that
+// share c begins inside of, if share c is the first to: 128 rows, a thread each, of 8 columns (y: column
+// and row blocks).
 constexpr int JOIN_COLS = 8;
 template <typename T>
 __global__ void __launch_bounds__(JOIN_THREADS) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u, int n1,

@@ -526,6 +526,7 @@ rlt_status paged_launchable(const rlt_model* m, const rlt_paged_batch* p, int n_
     int dev = -1;
     CK(cudaGetDevice(&dev));
     if (dev != m->device) return RLT_EINVAL;
+    if (p->max_kv > (1 << 29)) return RLT_EUNSUPPORTED;         // key counts are ints, with room to round up
     const long long heads = n_heads > p->n_kv_heads ? n_heads : p->n_kv_heads;
     if ((long long)p->N * heads + (long long)p->B * p->n_kv_heads > (1LL << 30)) return RLT_EUNSUPPORTED;
     return RLT_OK;

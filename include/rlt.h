@@ -29,7 +29,7 @@
  *     is the legacy default stream).  Argument errors are detected on the host before
  *     anything is launched and returned synchronously; nothing is then modified.
  *   - Device-side checks (token id out of range, a state that does not match its
- *     registered position) latch a flag in the model's device header; the next
+ *     registered position, a page outside its pool) latch a flag in the model's device header; the next
  *     rlt_last_error() call reports and clears it.
  *   - A model handle is not re-entrant: calls on one handle must be serialised by the
  *     caller.  Distinct handles are independent.
@@ -230,8 +230,8 @@ size_t rlt_page_pool_bytes(const rlt_model* m, int n_pages, int page_size, int n
  *   src_dtype   of k, v and q: RLT_F32, or RLT_BF16 in a bf16 model
  * Pointers 16-byte aligned, strides multiples of 8 and at least a row long.  A row's heads are
  * contiguous; q, k and v may be column ranges of one projection.  q_out may be q itself (same
- * type and stride).  One launch.  Errors: RLT_EINVAL, RLT_EUNSUPPORTED (N * n_heads beyond 2^30),
- * RLT_ECUDA. */
+ * type and stride).  One launch.  Errors: RLT_EINVAL, RLT_EUNSUPPORTED (N * n_heads beyond 2^30
+ * or max_kv beyond 2^29), RLT_ECUDA. */
 rlt_status rlt_paged_append(rlt_model* m, const rlt_paged_batch* p, void* pool, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, const void* q, int64_t q_stride, int n_heads,
                             void* q_out, int64_t q_out_stride, int src_dtype, void* stream);
@@ -252,7 +252,7 @@ size_t rlt_paged_attention_workspace_bytes(const rlt_model* m, const rlt_paged_b
  *   ws          rlt_paged_attention_workspace_bytes(m, p, n_heads) bytes; calls that may overlap
  *               on the GPU need workspaces of their own
  * Errors: RLT_EINVAL, RLT_EUNSUPPORTED (n_heads not a multiple of n_kv_heads, more than 64 query
- * heads per key head, N * n_heads beyond 2^30), RLT_ECUDA. */
+ * heads per key head, N * n_heads beyond 2^30, max_kv beyond 2^29), RLT_ECUDA. */
 rlt_status rlt_paged_attention(rlt_model* m, const rlt_paged_batch* p, const void* pool, const void* q,
                                int64_t q_stride, int n_heads, void* out, int64_t out_stride, float scale, void* ws,
                                size_t ws_bytes, void* stream);
@@ -453,7 +453,8 @@ rlt_status rlt_replay(rlt_model* m, const int32_t* tokens, int B, int T,
                       void* final_state, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then return and clear the device-side error flags:
- * RLT_OK, RLT_EDEVICE (bad token id or state/registry mismatch) or RLT_ETIMEOUT. */
+ * RLT_OK, RLT_EDEVICE (bad token id, state/registry mismatch, a page or lengths outside a paged
+ * batch's bounds, logits parameters out of range or a row left without a token) or RLT_ETIMEOUT. */
 rlt_status rlt_last_error(rlt_model* m, void* stream);
 
 /* Number of kernels the library has launched since the model was created (all entry

@@ -127,6 +127,12 @@ ATTEND = [
     ("bf16", 2, 2, 64, 256, [700, 65], [3000, 65], 0),
     ("bf16", 2, 1, 128, 64, [40], [20000], 0),
     ("bf16", 1, 1, 64, 128, [1], [30000], 0),
+    # many sequences: more than a warp, and more than a block, looks at in one go
+    ("bf16", 6, 2, 64, 16, [(0, 1, 2, 30, 0, 1, 9)[i % 7] for i in range(700)], [(i * 37) % 290 + 31 for i in range(700)], 4),
+    ("bf16", 4, 4, 128, 32, [1 + i % 2 for i in range(90)], [(i * 131) % 2000 + 2 for i in range(90)], 0),
+    # more tiles than a warp looks at in one go, of a group that does not divide a tile
+    ("bf16", 3, 1, 64, 64, [1, 5000, 40], [7000, 9000, 40], 1),
+    ("f32", 2, 2, 16, 16, [i % 3 for i in range(100)], [(i * 53) % 500 + 3 for i in range(100)], 2),
     ("f32", 4, 4, 16, 16, [1, 9, 100], [400, 9, 250], 1),
     ("f32", 6, 2, 32, 32, [1, 1], [5000, 3], 0),
     ("f32", 2, 1, 64, 64, [33, 1], [33, 900], 0),
@@ -168,7 +174,7 @@ def test_attention_matches_the_definition(case):
     assert torch.equal(again, out)
 
 
-@pytest.mark.parametrize("case", [ATTEND[3], ATTEND[8], ATTEND[15]], ids=["step", "chunk", "f32"])
+@pytest.mark.parametrize("case", [ATTEND[3], ATTEND[8], ATTEND[19]], ids=["step", "chunk", "f32"])
 def test_attention_takes_strided_rows_a_scale_and_large_scores(case):
     r, model, pool, q = attend_case(case, seed=7, scale_q=30.0, garbage=float("inf"))
     H, hd = q.shape[1:]
@@ -309,6 +315,34 @@ def test_bad_pages_and_lengths_are_latched_and_leave_the_rest_right():
             p, s = good.place(b, t)
             assert torch.equal(other[p, :, :, s], pool[p, :, :, s])
     assert model.last_error() == 0
+
+
+@pytest.mark.parametrize("dtype,hd,rows", [("bf16", 64, 5), ("bf16", 128, 40), ("f32", 32, 5)])
+def test_starts_that_overlap_are_latched_and_nothing_else_is_touched(dtype, hd, rows):
+    """Starts that go back and forth count the same rows many times, more than the host sized for; the
+    kernels leave out what does not fit, and the handle stays usable."""
+    H, Hkv, page, kv, B = 4, 2, 16, 3000, 64
+    model = op_model(dtype, hd, kv)
+    cols = -(-kv // page)
+    pool = randn((cols, 2, Hkv, page, hd), TYPES[dtype], 1)
+    table = torch.arange(cols, dtype=torch.int32, device="cuda").repeat(B, 1)
+    starts = torch.tensor([0, rows] * (B // 2) + [0], dtype=torch.int32, device="cuda")
+    kv_len = torch.full((B,), kv, dtype=torch.int32, device="cuda")
+    whole = randn((rows + 64, H, hd), TYPES[dtype], 2)
+    out = torch.full_like(whole, 3.0)
+    batch = model.paged_batch(table, starts, kv_len, rows, rows, kv, page, Hkv)
+    before = pool.clone()
+    model.paged_attention(batch, pool, whole[:rows], out=out[:rows])
+    assert model.last_error() == RLT_EDEVICE
+    assert bool((out[rows:] == 3.0).all()) and torch.equal(pool, before)
+    good = model.paged_batch(table[:1], torch.tensor([0, rows], dtype=torch.int32, device="cuda"), kv_len[:1], rows, rows, kv,
+                             page, Hkv)
+    r = Ragged([rows], [kv], page, n_pages=cols)
+    r.table_np[0] = np.arange(cols)
+    got = model.paged_attention(good, pool, whole[:rows])
+    assert model.last_error() == 0
+    ref, tol = attention_ref(pool, r, whole[:rows])
+    assert bool(((got.double() - ref).abs() <= tol).all())
 
 
 def test_refusals():
