@@ -54,11 +54,11 @@ __device__ __forceinline__ void load_w(const float* p, float* x) {
 }
 
 // LT threads with EPT elements each, in vectors of 4 (VEC) or one by one.  AHEAD: the next row's
-// elements are fetched into shared memory (where that has room).
+// elements are fetched into shared memory (where that has room; one by one, each has a mask word too).
 template <int LT, int EPT, bool VEC>
 struct LogitsShape {
     static constexpr int W = VEC ? 4 : 1;
-    static constexpr bool AHEAD = LT * EPT <= 16384;
+    static constexpr bool AHEAD = LT * EPT <= (VEC ? 16384 : 8192);
     static constexpr int CTAS = LT == 256 ? 4 : (LT * EPT <= 8192 ? 2 : 1);
     // counters; x, bias, mask words (one per vector) and a token per thread of the next row
     static size_t smem(int slice, bool history, bool bias) {

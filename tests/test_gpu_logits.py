@@ -179,6 +179,25 @@ def test_strides_and_alignment(offset):
     assert bool((whole == 77).all())
 
 
+@pytest.mark.parametrize("V,B", [(512, 2), (2000, 3), (8000, 300), (20000, 160), (30000, 2), (60000, 2), (200000, 1)])
+def test_unaligned_rows_of_every_size(V, B):
+    """Rows at odd addresses, with all that a call can have, for every split of a row."""
+    hist = 40
+    model = op_model("f32", 16, 8, V=V)
+    r, x, tokens, tok_len, gen, par = inputs(B, V, hist, 9)
+    bias = (r.standard_normal((B, V)) * (r.random((B, V)) < 0.2)).astype(np.float32)
+    allowed = r.random((B, V)) < 0.5
+    allowed[:, 1] = True
+    want, _, tol = reference(x, bias=bias, allowed=allowed, tokens=tokens, tok_len=tok_len, gen_start=gen, **par)
+    rows = [torch.zeros((B, V + 3), device="cuda")[:, 1:V + 1] for _ in range(3)]
+    rows[0].copy_(torch.from_numpy(x))
+    rows[1].copy_(torch.from_numpy(bias))
+    model.process_logits(rows[0], out=rows[2], bias=rows[1], mask=bits(allowed), tokens=dev(tokens), tok_len=dev(tok_len),
+                         gen_start=dev(gen), **{k: dev(v) for k, v in par.items()})
+    assert model.last_error() == 0
+    check(rows[2], want, tol)
+
+
 def test_what_masked_places_hold_does_not_matter():
     V, B = 2056, 4
     model = op_model("f32", 16, 8, V=V)
