@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
         const float safe = m == -INFINITY ? 0.f : m;            // nothing allowed here: every term is exp(-inf)
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) s += ex2_approx(fmaf(x[i], LOG2E, -safe * LOG2E));
+        for (int i = 0; i < EPT; ++i) s += ex2_approx((x[i] - safe) * LOG2E);       // (safe * LOG2E may overflow)
         s = warp_sum(s);
         float2* all = pairs[round & 1];
         if (n_cta > 1) {
@@ -212,12 +212,12 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
         s = warp_sum(s);
         // No token allowed: all -inf.  (A NaN leaves no sum of zero, and the row is NaN.)
         const bool empty = m == -INFINITY && s == 0.f;
-        const float lse = empty ? -INFINITY : m + logf(s);
+        const float log_s = empty ? 0.f : logf(s);
         if (rank == 0 && tid == 0) {
-            if (a.out_lse) a.out_lse[b] = lse;
+            if (a.out_lse) a.out_lse[b] = m + log_s;
             if (empty) raise_flag(a.hdr, ERR_BAD_LOGITS);
         }
-        const float less = empty ? 0.f : lse;                   // (an empty row's elements are -inf as they are)
+        if (empty) m = 0.f;                                     // (its elements are -inf as they are)
         float* o = a.out + b * a.out_stride + v0;
 #pragma unroll
         for (int i = 0; i < EPT; i += W) {
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
             if (e >= n) continue;
             float y[W];
 #pragma unroll
-            for (int j = 0; j < W; ++j) y[j] = x[i + j] - less;
+            for (int j = 0; j < W; ++j) y[j] = x[i + j] - m - log_s;      // (m + log_s may round log_s away)
             if (VEC)
                 __stcs(reinterpret_cast<float4*>(o + e), make_float4(y[0], y[W > 1 ? 1 : 0], y[W > 2 ? 2 : 0], y[W > 2 ? 3 : 0]));
             else

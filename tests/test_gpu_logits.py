@@ -198,6 +198,25 @@ def test_unaligned_rows_of_every_size(V, B):
     check(rows[2], want, tol)
 
 
+@pytest.mark.parametrize("V,B", [(520, 3), (32768, 2), (16384, 300)])
+def test_rows_of_the_types_lowest_and_highest_value(V, B):
+    """A row of equal values is uniform whatever they are: V ones add up exactly, their logarithm is off
+    by an ulp, and the difference rounds once."""
+    model = op_model("f32", 16, 8, V=V)
+    x = np.zeros((B, V), np.float32)
+    top = np.float32(3.4028235e38)
+    tol = 2.0 ** -22 * np.log(V)
+    for value in (-top, top, np.float32(-1e30), np.float32(1e4)):
+        got = to_np(model.process_logits(dev(x + value)))
+        assert np.abs(got + np.log(V)).max() <= tol
+        got = to_np(model.process_logits(dev(x), bias=dev(x[:1] + value)))
+        assert np.abs(got + np.log(V)).max() <= tol
+    x[:, ::2], x[:, 1::2] = top, -top
+    got = to_np(model.process_logits(dev(x)))
+    assert np.abs(got[:, ::2] + np.log(V / 2)).max() <= tol and (got[:, 1::2] < -1e38).all()
+    assert model.last_error() == 0
+
+
 def test_what_masked_places_hold_does_not_matter():
     V, B = 2056, 4
     model = op_model("f32", 16, 8, V=V)
