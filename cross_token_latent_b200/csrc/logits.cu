@@ -7,15 +7,19 @@
 //   z = z + bias;  z = -inf where the mask's bit is 0;  z = z / tau
 //   out = z - log sum exp z
 //
-// Eight bytes per element (and four with a bias of every row) have to move; memory bounds it.  A
-// row is cut over a cluster of CTAs, each of which keeps its share in registers between the two
-// halves of the softmax, so the row is read once; every warp's (maximum, sum) goes to all CTAs of the
-// cluster by distributed shared memory, and one cluster barrier per row joins them.  The clusters walk
-// through the rows, and a thread's elements of the next row are on their way (cp.async, into places
-// that only it reads) while this one's are reduced and written; a CTA per share without that spent
-// most of its time waiting for its own loads (512 rows of 32768 with everything: 76 us).
-// The history is counted into shared memory with integer atomics, whose order cannot change a
-// count: bit 31 is set for a token seen anywhere, the bits below count the later part.
+// Eight bytes per element (and four with a bias of every row) have to move; memory bounds it where rows
+// are many, and the chain of steps per row where they are few.  A row is cut over a cluster of CTAs,
+// each of which keeps its share in registers between the two halves of the softmax, so the row is read
+// once; every warp's (maximum, sum) goes to all CTAs of the cluster by distributed shared memory, and one
+// cluster barrier per row joins them.  The clusters walk through the rows, and a thread's elements of the
+// next row are on their way (cp.async) while this one's are reduced and written.  Two CTAs per SM work
+// while the other waits, and few threads with many elements each spend less on what a row costs a warp:
+// 512 rows of 32768 with everything take 42 us by pairs of 256 threads with 64 elements each, 44 by 1024
+// with 16, one CTA per SM, and 76 without the copies ahead.
+//
+// The history is counted into shared memory with integer atomics, whose order cannot change a count.
+// Of a token's occurrences the one that comes first then changes its logit, so that the steps over the
+// whole row know nothing of penalties (looking at every element's counter took 47 us in place of 44).
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -24,7 +28,10 @@ namespace rlt {
 namespace {
 
 constexpr int MAX_CLUSTER = 8;
-constexpr uint32_t SEEN = 0x80000000u;
+constexpr uint32_t SEEN = 0x80000000u;      // in a counter of 32 bits
+constexpr uint32_t DONE = 0xffffu;          // in one of 16 bits, which counts up to MAX_COUNT
+constexpr int MAX_COUNT = 0xfffe;
+constexpr int TOKENS = 1024;                // of a history, fetched ahead
 
 constexpr float LOG2E = 1.4426950408889634f;
 // 2^x by the ex2.approx instruction (relative error ~2^-22), a term of a sum only
@@ -54,99 +61,138 @@ __device__ __forceinline__ void load_w(const float* p, float* x) {
 }
 
 // LT threads with EPT elements each, in vectors of 4 (VEC) or one by one.  AHEAD: the next row's
-// elements are fetched into shared memory (where that has room; one by one, each has a mask word too).
+// elements are fetched into shared memory (where that has room), and counters have 16 bits.
 template <int LT, int EPT, bool VEC>
 struct LogitsShape {
     static constexpr int W = VEC ? 4 : 1;
-    static constexpr bool AHEAD = LT * EPT <= (VEC ? 16384 : 8192);
-    static constexpr int CTAS = LT == 256 ? 4 : (LT * EPT <= 8192 ? 2 : 1);
-    // counters; x, bias, mask words (one per vector) and a token per thread of the next row
+    static constexpr bool AHEAD = LT * EPT <= 16384;
+    static constexpr bool BIAS = LT * EPT <= 8192;              // the bias too
+    static constexpr int CTAS = LT * EPT <= 4096 ? 4 : (LT * EPT <= 16384 ? 2 : 1);
+    static constexpr int WORDS = LT * EPT / 32;                 // of the mask
+    // counters; x, bias, mask words (of two rows) and the first tokens of the next row
     static size_t smem(int slice, bool history, bool bias) {
-        return (size_t)slice * 4 * ((history ? 1 : 0) + (AHEAD ? 1 : 0) + (bias && AHEAD ? 1 : 0)) +
-               (AHEAD ? (size_t)LT * (EPT / W + 1) * 4 : 0);
+        return (size_t)slice * ((history ? (AHEAD ? 2 : 4) : 0) + (AHEAD ? 4 : 0) + (bias && BIAS ? 4 : 0)) +
+               (AHEAD ? (size_t)(2 * WORDS + TOKENS) * 4 : 0);
     }
 };
+
+// What a call asks of a row.
+struct LogitsRow {
+    float rep, tau, presence, frequency, lse;
+    int len, gen;
+};
+__device__ __forceinline__ LogitsRow load_row(const LogitsArgs& a, int b) {
+    return {a.repetition ? a.repetition[b] : 1.f, a.tau ? a.tau[b] : 1.f, a.presence ? a.presence[b] : 0.f,
+            a.frequency ? a.frequency[b] : 0.f, a.lse ? a.lse[b] : 0.f, a.tok_len ? a.tok_len[b] : a.n_tokens,
+            a.gen_start ? a.gen_start[b] : 0};
+}
 
 template <int LT, int EPT, bool VEC>
 __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process_logits(LogitsArgs a, int slice, int n_cta) {
     using S = LogitsShape<LT, EPT, VEC>;
     constexpr int W = S::W, LW = LT / 32;
     extern __shared__ __align__(16) uint32_t count[];           // [slice] with a history
-    float* ahead = reinterpret_cast<float*>(count + (a.tokens ? slice : 0));        // [slice] x of the next row
+    uint16_t* const count16 = reinterpret_cast<uint16_t*>(count);
+    float* ahead = reinterpret_cast<float*>(count + (a.tokens ? slice / 2 : 0));    // [slice] x of the next row
     float* bias_sm = ahead + slice;                             // [slice] its bias, or every row's
-    uint32_t* mask_sm = reinterpret_cast<uint32_t*>(bias_sm + (a.bias ? slice : 0));    // [EPT / W][LT] its mask words
-    int32_t* token_sm = reinterpret_cast<int32_t*>(mask_sm + EPT / W * LT);             // [LT] its first tokens
+    // [2][WORDS] mask words, by the row's parity
+    uint32_t* mask_sm = reinterpret_cast<uint32_t*>(bias_sm + (S::BIAS && a.bias ? slice : 0));
+    int32_t* token_sm = reinterpret_cast<int32_t*>(mask_sm + 2 * S::WORDS);             // [TOKENS] its first tokens
     __shared__ float2 pairs[2][MAX_CLUSTER * LW];               // of all warps of the cluster, by the row's parity
     const int rank = n_cta > 1 ? (int)cluster_rank() : 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int v0 = rank * slice, n = max(0, min(slice, a.V - v0));
     const int clusters = gridDim.x / n_cta;
     if (a.tokens)
-        for (int i = tid; i < slice; i += LT) count[i] = 0;
+        for (int i = tid; i < (S::AHEAD ? slice / 2 : slice); i += LT) count[i] = 0;
     // a peer's shared memory may be written once the peer runs: the wait is before the first exchange
     if (n_cta > 1) cluster_arrive_release();
     pdl_wait();
     pdl_trigger();
 
     const bool own_bias = a.bias && a.bias_stride != 0;         // a bias of every row
-    auto fetch = [&](long long b, bool bias_too) {
+    auto fetch = [&](long long b, int parity, bool bias_too) {
+        const float* x = a.x + b * a.x_stride + v0 + tid * W;
+        const float* bias = a.bias + b * a.bias_stride + v0 + tid * W;
 #pragma unroll
         for (int i = 0; i < EPT; i += W) {
-            const int e = i * LT + tid * W;
-            if (e >= n) continue;
-            cp_async<4 * W>(ahead + e, a.x + b * a.x_stride + v0 + e);
-            if (bias_too) cp_async<4 * W>(bias_sm + e, a.bias + b * a.bias_stride + v0 + e);
-            if (a.mask) cp_async<4>(mask_sm + i / W * LT + tid, a.mask + b * a.mask_stride + ((v0 + e) >> 5));
+            if (i * LT + tid * W >= n) continue;
+            cp_async<4 * W>(ahead + tid * W + i * LT, x + i * LT);
+            if (S::BIAS && bias_too) cp_async<4 * W>(bias_sm + tid * W + i * LT, bias + i * LT);
         }
-        if (a.tokens && tid < a.n_tokens) cp_async<4>(token_sm + tid, a.tokens + b * a.seq_stride + tid * a.tok_stride);
+        if (a.mask)
+            for (int i = tid; i * 32 < n; i += LT)
+                cp_async<4>(mask_sm + parity * S::WORDS + i, a.mask + b * a.mask_stride + (v0 >> 5) + i);
+        if (a.tokens)
+            for (int i = tid; i < min(a.n_tokens, TOKENS); i += LT)
+                cp_async<4>(token_sm + i, a.tokens + b * a.seq_stride + i * a.tok_stride);
     };
     int b = blockIdx.x / n_cta;
-    if (S::AHEAD) fetch(b, a.bias != nullptr);
+    if (S::AHEAD) fetch(b, 0, a.bias != nullptr);
+    LogitsRow row = load_row(a, b);
     if (n_cta > 1) cluster_wait_acquire();
     else __syncthreads();                                       // the counters are zero
 
     for (int round = 0; b < a.B; b += clusters, ++round) {
-        float rep = a.repetition ? a.repetition[b] : 1.f, tau = a.tau ? a.tau[b] : 1.f;
-        const float presence = a.presence ? a.presence[b] : 0.f, frequency = a.frequency ? a.frequency[b] : 0.f;
-        const float lse_in = a.lse ? a.lse[b] : 0.f;
         bool bad = false;
-        if (!(rep > 0.f)) { rep = 1.f; bad = true; }
-        if (!(tau > 0.f)) { tau = 1.f; bad = true; }
-        if (S::AHEAD) cp_async_wait();                          // this thread's own elements
-        if (a.tokens) {
-            int len = a.tok_len ? a.tok_len[b] : a.n_tokens;
-            if (len < 0 || len > a.n_tokens) { len = min(max(len, 0), a.n_tokens); bad = true; }
-            const int gen = a.gen_start ? a.gen_start[b] : 0;
-            const int32_t* t = a.tokens + b * a.seq_stride;
-#pragma unroll 4
-            for (int i = tid; i < len; i += LT) {
-                const int id = S::AHEAD && i == tid ? token_sm[tid] : t[i * a.tok_stride], e = id - v0;
+        if (!(row.rep > 0.f)) { row.rep = 1.f; bad = true; }
+        if (!(row.tau > 0.f)) { row.tau = 1.f; bad = true; }
+        if (row.len < 0 || row.len > a.n_tokens) { row.len = min(max(row.len, 0), a.n_tokens); bad = a.tokens || bad; }
+        const float inv_tau = 1.0f / row.tau, inv_rep = 1.0f / row.rep, lse_in = row.lse;
+        // Less the input's log-sum-exp, as x is: only penalties need it, the softmax does not.
+        auto penalise = [&](float x, uint32_t c) {
+            x += lse_in;
+            x *= x > 0.f ? inv_rep : row.rep;
+            if (c > 0) x -= row.presence + row.frequency * (float)c;
+            return x - lse_in;
+        };
+        const int32_t* t = a.tokens + b * a.seq_stride;
+        auto each_token = [&](auto&& visit) {                   // of the history, in this CTA's share
+#pragma unroll 2
+            for (int i = tid; i < row.len; i += LT) {
+                const int id = S::AHEAD && i < TOKENS ? token_sm[i] : t[i * a.tok_stride], e = id - v0;
                 if (id < 0 || id >= a.V) bad = true;
-                else if (e >= 0 && e < n) {
-                    if (i >= gen) atomicAdd(&count[e], 1u);
+                else if (e >= 0 && e < n) visit(i, e);
+            }
+        };
+        if (S::AHEAD) cp_async_wait();
+        if (a.tokens) {
+            each_token([&](int i, int e) {
+                if (S::AHEAD) {
+                    if (i >= row.gen) atomicAdd(&count[e >> 1], 1u << 16 * (e & 1));
+                } else {
+                    if (i >= row.gen) atomicAdd(&count[e], 1u);
                     atomicOr(&count[e], SEEN);
                 }
+            });
+            __syncthreads();
+            if (S::AHEAD) {
+                // whoever of a token's occurrences comes first sees to it
+                each_token([&](int, int e) {
+                    const uint32_t c = atomicOr(&count[e >> 1], DONE << 16 * (e & 1)) >> 16 * (e & 1) & DONE;
+                    if (c != DONE) ahead[e] = penalise(ahead[e], c);
+                });
+                __syncthreads();
+                each_token([&](int, int e) { count16[e] = 0; });        // for the next row
             }
+        } else if (S::AHEAD && a.mask) {
             __syncthreads();
         }
         if (bad) raise_flag(a.hdr, ERR_BAD_LOGITS);
 
-        const float inv_tau = 1.0f / tau, inv_rep = 1.0f / rep;
+        // Steps without a branch per element: what lies behind the share is read too, from somewhere in
+        // it, and made -inf at the end.
         float x[EPT];
-        float m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < EPT; i += W) {
             const int e = i * LT + tid * W;
+            if (S::AHEAD) {
+                load_w<W>(ahead + min(e, slice - W), x + i);
+            } else {
 #pragma unroll
-            for (int j = 0; j < W; ++j) x[i + j] = 0.f;
-            // the W elements of a vector lie in one word of the mask: their first id is a multiple of W
-            uint32_t bits = e < n ? 0xfu : 0u;
-            if (e < n) {
-                if (a.mask) bits = (S::AHEAD ? mask_sm[i / W * LT + tid] : a.mask[b * a.mask_stride + ((v0 + e) >> 5)]) >> ((v0 + e) & 31);
-                load_w<W>(S::AHEAD ? ahead + e : a.x + b * a.x_stride + v0 + e, x + i);
-#pragma unroll
-                for (int j = 0; j < W; ++j) x[i + j] += lse_in;
-                if (a.tokens) {
+                for (int j = 0; j < W; ++j) x[i + j] = 0.f;
+                if (e < n) load_w<W>(a.x + b * a.x_stride + v0 + e, x + i);
+                if (e < n && a.tokens) {
                     uint32_t c[W], any = 0;
                     load_w<W>(reinterpret_cast<const float*>(count) + e, reinterpret_cast<float*>(c));
 #pragma unroll
@@ -155,34 +201,70 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
 #pragma unroll
                         for (int j = 0; j < W; ++j) {
                             if (c[j]) {
-                                x[i + j] *= x[i + j] > 0.f ? inv_rep : rep;
-                                if (c[j] != SEEN) x[i + j] -= presence + frequency * (float)(c[j] & ~SEEN);
+                                x[i + j] = penalise(x[i + j], c[j] & ~SEEN);
                                 count[e + j] = 0;               // for the next row
                             }
                         }
                     }
                 }
-                if (a.bias) {
-                    float bi[W];
-                    load_w<W>(S::AHEAD ? bias_sm + e : a.bias + b * a.bias_stride + v0 + e, bi);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) x[i + j] += bi[j];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                x[i + j] = bits & (1u << j) ? x[i + j] * inv_tau : -INFINITY;
-                m = fmaxf(m, x[i + j]);
             }
         }
-        if (S::AHEAD && b + clusters < a.B) fetch(b + clusters, own_bias);
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < EPT; i += W) {
+                const int e = i * LT + tid * W;
+                float bi[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j) bi[j] = 0.f;
+                if (S::BIAS) load_w<W>(bias_sm + min(e, slice - W), bi);
+                else if (e < n) load_w<W>(a.bias + b * a.bias_stride + v0 + e, bi);
+#pragma unroll
+                for (int j = 0; j < W; ++j) x[i + j] += bi[j];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < EPT; i += 2) {
+            const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(inv_tau, inv_tau));
+            x[i] = y.x;
+            x[i + 1] = y.y;
+        }
+        if (a.mask) {
+#pragma unroll
+            for (int i = 0; i < EPT; i += W) {
+                // the W elements of a vector lie in one word: their first id is a multiple of W
+                const int e = i * LT + tid * W;
+                uint32_t word = 0;
+                if (S::AHEAD) word = mask_sm[(round & 1) * S::WORDS + (e >> 5)];
+                else if (e < n) word = a.mask[b * a.mask_stride + ((v0 + e) >> 5)];
+                word >>= tid * W & 31;
+#pragma unroll
+                for (int j = 0; j < W; ++j) x[i + j] = word & (1u << j) ? x[i + j] : -INFINITY;
+            }
+        }
+        if (n < LT * EPT) {
+#pragma unroll
+            for (int i = 0; i < EPT; i += W)
+#pragma unroll
+                for (int j = 0; j < W; ++j) x[i + j] = i * LT + tid * W < n ? x[i + j] : -INFINITY;
+        }
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) m = fmaxf(m, x[i]);
+        if (b + clusters < a.B) {
+            if (S::AHEAD) fetch(b + clusters, (round + 1) & 1, own_bias);
+            row = load_row(a, b + clusters);
+        }
 
         m = warp_max(m);
         const float safe = m == -INFINITY ? 0.f : m;            // nothing allowed here: every term is exp(-inf)
-        float s = 0.f;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) s += ex2_approx((x[i] - safe) * LOG2E);       // (safe * LOG2E may overflow)
-        s = warp_sum(s);
+        for (int i = 0; i < EPT; i += 2) {
+            // (safe * LOG2E may overflow)
+            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-safe, -safe)), make_float2(LOG2E, LOG2E));
+            sum = add2(sum, make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+        }
+        float s = warp_sum(sum.x + sum.y);
         float2* all = pairs[round & 1];
         if (n_cta > 1) {
             if (lane < n_cta) {
@@ -197,24 +279,17 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
         }
         // every warp joins the pairs alike
         m = -INFINITY;
-        float2 mine[(MAX_CLUSTER * LW + 31) / 32];
-#pragma unroll
-        for (int k = 0; k < (MAX_CLUSTER * LW + 31) / 32; ++k) {
-            const int i = k * 32 + lane;
-            mine[k] = i < n_cta * LW ? all[i] : make_float2(-INFINITY, 0.f);
-            m = fmaxf(m, mine[k].x);
-        }
+        for (int i = lane; i < n_cta * LW; i += 32) m = fmaxf(m, all[i].x);
         m = warp_max(m);
         const float top = m == -INFINITY ? 0.f : m;
         s = 0.f;
-#pragma unroll
-        for (int k = 0; k < (MAX_CLUSTER * LW + 31) / 32; ++k) s += mine[k].y * ex2_approx((mine[k].x - top) * LOG2E);
+        for (int i = lane; i < n_cta * LW; i += 32) s += all[i].y * ex2_approx((all[i].x - top) * LOG2E);
         s = warp_sum(s);
         // No token allowed: all -inf.  (A NaN leaves no sum of zero, and the row is NaN.)
         const bool empty = m == -INFINITY && s == 0.f;
-        const float log_s = empty ? 0.f : logf(s);
+        const float log_s = (empty ? 0.f : logf(s)) + (lse_in - lse_in);        // (NaN where lse is)
         if (rank == 0 && tid == 0) {
-            if (a.out_lse) a.out_lse[b] = m + log_s;
+            if (a.out_lse) a.out_lse[b] = m + log_s + lse_in * inv_tau;
             if (empty) raise_flag(a.hdr, ERR_BAD_LOGITS);
         }
         if (empty) m = 0.f;                                     // (its elements are -inf as they are)
@@ -223,13 +298,15 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
         for (int i = 0; i < EPT; i += W) {
             const int e = i * LT + tid * W;
             if (e >= n) continue;
-            float y[W];
-#pragma unroll
-            for (int j = 0; j < W; ++j) y[j] = x[i + j] - m - log_s;      // (m + log_s may round log_s away)
-            if (VEC)
-                __stcs(reinterpret_cast<float4*>(o + e), make_float4(y[0], y[W > 1 ? 1 : 0], y[W > 2 ? 2 : 0], y[W > 2 ? 3 : 0]));
-            else
-                o[e] = y[0];
+            // (m + log_s may round log_s away)
+            if (VEC) {
+                const float2 mm = make_float2(-m, -m), ll = make_float2(-log_s, -log_s);
+                const float2 y0 = add2(add2(make_float2(x[i], x[i + 1]), mm), ll);
+                const float2 y1 = add2(add2(make_float2(x[i + W / 2], x[i + W - 1]), mm), ll);
+                __stcs(reinterpret_cast<float4*>(o + e), make_float4(y0.x, y0.y, y1.x, y1.y));
+            } else {
+                o[e] = x[i] - m - log_s;
+            }
         }
     }
 }
@@ -274,14 +351,19 @@ cudaError_t launch_process_logits(Launch L, const LogitsArgs& a) {
     const bool vec = a.V % 4 == 0 && al(a.x, a.x_stride) && al(a.out, a.out_stride) &&
                      (!a.bias || al(a.bias, a.bias_stride));
     const auto share = [&](int c) { return ((a.V + c - 1) / c + 31) / 32 * 32; };
-    // Every CTA more in a row's cluster costs time at its barrier (512 rows of 32768 with everything: 8
-    // CTAs of 256 threads 70 us, 4 of 512 the same, 2 of 1024 50 us), so rows are cut as little as
-    // possible where there are enough of them for every SM ...
+    // Counters of 16 bits could overflow.
+    if (a.tokens && a.n_tokens > MAX_COUNT) {
+        const int c = (a.V + 32767) / 32768;
+        return vec ? run<512, 64, true>(L, a, c, share(c)) : run<512, 64, false>(L, a, c, share(c));
+    }
+    // Every CTA more in a row's cluster costs time at its barrier (512 rows of 32768 with everything: 4
+    // CTAs of 256 threads 54 us, 2 of them 42 us), so rows are cut as little as possible where there are
+    // enough of them for every SM ...
     const int c1 = (a.V + 16383) / 16384;
     if (a.V > 2048 && a.V <= 8192 && a.B >= 2 * sm_count())
         return vec ? run<512, 16, true>(L, a, 1, share(1)) : run<512, 16, false>(L, a, 1, share(1));
     if (a.V > 2048 && c1 <= MAX_CLUSTER && (long long)a.B * c1 >= sm_count())
-        return vec ? run<1024, 16, true>(L, a, c1, share(c1)) : run<1024, 16, false>(L, a, c1, share(c1));
+        return vec ? run<256, 64, true>(L, a, c1, share(c1)) : run<256, 64, false>(L, a, c1, share(c1));
     // ... and else until there are two CTAs of 256 threads per SM, while every thread keeps 8 elements
     // (64 rows of 32000: 9 us against 13 us).
     int c = (a.V + 4095) / 4096;

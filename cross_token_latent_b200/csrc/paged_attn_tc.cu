@@ -1,6 +1,6 @@
 // Attention of many new rows over a paged cache on the sm_100a tensor cores (bf16, head_dim 64 or
-// 128).  One CTA per SM takes an equal share of all the work (paged.cuh) and walks through the items
-// in it.  An item is a tile of one key head's rows, two stages of up to 128 (rows of a group of query
+// 128).  A CTA (one per SM, two at head width 64) takes an equal share of all the work (paged.cuh) and
+// walks through the items in it.  An item is a tile of one key head's rows, two stages of up to 128 (rows of a group of query
 // heads beside each other, so that shared keys are read once), against key tiles of 128:
 //   warps 0-3    softmax of stage 0, warps 4-7 of stage 1, a thread per row: the scores leave TMEM
 //                once, P_s goes back as bf16 over the scores' own columns
@@ -43,7 +43,7 @@ struct TcShape {
     static constexpr int OFF_KV = STAGES * Q_BYTES;
     static constexpr int OFF_BAR = OFF_KV + SLOTS * T_BYTES;
     static constexpr int SMEM = OFF_BAR + 256 + 1024;
-    static constexpr int POLY = HD == 128 ? 2 : 2;          // of 8 exponentials, those not on the special function unit
+    static constexpr int POLY = 2;                          // of 8 exponentials, those not on the special function unit
     static constexpr uint32_t O_COL = STAGES * KH;          // O behind the scores
     static constexpr uint32_t TMEM_COLS = STAGES * (KH + HD);
     static constexpr int SOFTMAX_WARPS = 4 * STAGES;
@@ -63,26 +63,6 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
     return ok != 0;
-}
-
-// Two float32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
 }
 
 // 2^x for two x in [-125, 0] and a little above on the multiply-add units: x = n + f with n the nearest
@@ -154,7 +134,7 @@ struct Walk {
     int tiles, steps;           // of the sequence; of the item
     long long left;             // steps of the share, this stretch's among them
 
-    __device__ __forceinline__ void enter(const PagedArgs&, const SharePlan& u) {
+    __device__ __forceinline__ void enter(const SharePlan& u) {
         steps = share_steps(u, s, tile);
         n = (int)(left < steps - step ? left : steps - step);
     }
@@ -165,7 +145,7 @@ struct Walk {
         s = load_seq(p, b);
         tiles = share_tiles(u, s);
         locate_step(u, s, p.Hkv, st.off, tile, head, step);
-        enter(p, u);
+        enter(u);
     }
     __device__ __forceinline__ bool next(const PagedArgs& p, const SharePlan& u) {
         left -= n;
@@ -196,7 +176,7 @@ struct Walk {
                 tiles = share_tiles(u, s);
             }
         }
-        enter(p, u);
+        enter(u);
         return true;
     }
 };

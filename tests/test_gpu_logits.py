@@ -136,6 +136,21 @@ def test_matches_the_definition(V, B, hist, with_lse, bias_rows, with_mask):
     assert torch.equal(y, out)
 
 
+@pytest.mark.parametrize("V,n", [(512, 70000), (40000, 66000)])
+def test_a_long_history_of_one_token(V, n):
+    """More occurrences than 16 bits count, and as many as they do."""
+    model = op_model("f32", 16, 8, V=V)
+    r, x, _, _, _, par = inputs(2, V, 0, 10)
+    tokens = np.full((2, n), V - 3, np.int32)
+    tokens[:, :100] = r.integers(0, V, (2, 100))
+    for lens in ([n, n], [65534, 65000]):
+        for m in (n, max(lens)):
+            kw = dict(tokens=tokens[:, :m], tok_len=np.array(lens, np.int32), gen_start=np.array([0, 50], np.int32), **par)
+            want, _, tol = reference(x, **kw)
+            check(model.process_logits(dev(x), **{k: dev(v) for k, v in kw.items()}), want, tol)
+    assert model.last_error() == 0
+
+
 @pytest.mark.parametrize("only", ["repetition", "presence", "frequency", "tau", "none", "nothing but a history"])
 def test_each_parameter_alone(only):
     V, B = 512, 4
