@@ -158,15 +158,18 @@ inline unsigned rows_grid(long long n) {
 
 }  // namespace
 
-constexpr int ROW_BLOCKS = 16;          // per SM (32768 rows, heads of 128: 8 take 223 us, 16 take 201 us)
+// Threads per SM that walk through the rows (32768 rows, heads of 128: 2048 take 223 us, 4096 take 201 us).
+constexpr int ROW_THREADS = 4096;
 
 template <typename T, typename S>
 cudaError_t launch_paged_append(Launch L, const PagedArgs& p, const AppendArgs& a) {
     // 16 bytes per load: 4 float32 elements, 8 in bf16 (heads of 16 have halves of 8)
     constexpr int VEC = 16 / sizeof(S);
+    // Rows of few items have small blocks (42000 float32 rows of 40 items: 44 us in blocks of 256, 32 us in blocks of 64).
     const int items = (a.H + 2 * p.Hkv) * (a.hd / (2 * VEC)), chunks = (items + 255) / 256;
-    const int most = (ROW_BLOCKS * sm_count() + chunks - 1) / chunks;
-    return launch_k(L, k_paged_append<T, S, VEC>, dim3(p.N < most ? p.N : most, chunks), 256, 0, p, a);
+    const int threads = ((items + chunks - 1) / chunks + 31) / 32 * 32;
+    const int most = (ROW_THREADS * sm_count() + chunks * threads - 1) / (chunks * threads);
+    return launch_k(L, k_paged_append<T, S, VEC>, dim3(p.N < most ? p.N : most, chunks), threads, 0, p, a);
 }
 
 template <typename T>
