@@ -170,7 +170,9 @@ __device__ __forceinline__ bool find_unit(const PagedArgs& p, const UnitPlan& u,
 // sequence by sequence, tile by tile, head by head, key by key, cut into equal shares, one per
 // CTA.  A share begins and ends anywhere, so every CTA has the same work whatever the raggedness
 // and the causal order; an item (a tile and head) is cut only where a share ends, which leaves at
-// most two partial states per CTA.  With `whole` an item counts as one step and is never cut.
+// most two partial states per CTA.  A step counts the same whether its tile fills both of its stages of
+// rows or one: alone, a stage waits for its own chain (9 turns with heads of 64, steps of one stage
+// counted half: 122 us in place of 100).  With `whole` an item counts as one step and is never cut.
 constexpr int STEP_KEYS = 128;
 struct SharePlan {
     int g;                      // query heads per key head

@@ -316,11 +316,19 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             first = false;
             if (nh == 0) continue;
             const int limit = mine ? w.s.kv - w.s.nq + row / u.g - x_.k_begin : -1;    // last key, from the first
+            // Where two CTAs share an SM a warp without rows leaves its issue slots to the others; its rows of O
+            // hold anything.  (9 turns with heads of 64: 100 -> 98 us; with heads of 128, alone on its SM, 135
+            // -> 139 us.)
+            const bool idle = S::CTAS > 1 && !__any_sync(0xffffffffu, mine);
             float m = -INFINITY, l = 0.f;       // m of the scaled scores
             for (int h = 0; h < nh; ++h) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], s_phase, &abort_flag));
                 if (!ok) break;
                 s_phase ^= 1;
+                if (idle) {
+                    if (lane == 0) mbar_arrive(&p_full[s]);
+                    continue;
+                }
                 tc_fence_after();
                 const int seen = limit - h * S::KH;         // columns 0 .. seen of this block are seen
                 const bool masked = __any_sync(0xffffffffu, seen < S::KH - 1);
