@@ -357,27 +357,28 @@ cudaError_t launch_process_logits(Launch L, const LogitsArgs& a) {
         return vec ? run<512, 64, true>(L, a, c, share(c)) : run<512, 64, false>(L, a, c, share(c));
     }
     // Every CTA more in a row's cluster costs time at its barrier (512 rows of 32768 with everything: 4
-    // CTAs of 256 threads 54 us, 2 of them 42 us), so rows are cut as little as possible where there are
-    // enough of them for every SM ...
+    // CTAs of 256 threads 54 us, 2 of them 42 us), so rows are cut as little as possible where that gives
+    // every second SM a CTA (64 rows of 32000: 2 CTAs 8.9 us, 8 of them 9.9 us; 16 rows: 8.5 us, 6.5 us) ...
+    const auto enough = [&](int c) { return 2LL * a.B * c >= sm_count(); };
     const int c1 = (a.V + 16383) / 16384;
-    if (a.V > 2048 && a.V <= 8192 && a.B >= 2 * sm_count())
+    // (100 rows of 8192: one CTA 6.1 us, three 8.3 us; rows up to 4096 have smaller ones below)
+    if (a.V > 4096 && a.V <= 8192 && enough(1))
         return vec ? run<512, 16, true>(L, a, 1, share(1)) : run<512, 16, false>(L, a, 1, share(1));
-    if (a.V > 2048 && c1 <= MAX_CLUSTER && (long long)a.B * c1 >= sm_count())
+    if (a.V > 8192 && c1 <= MAX_CLUSTER && enough(c1))
         return vec ? run<256, 64, true>(L, a, c1, share(c1)) : run<256, 64, false>(L, a, c1, share(c1));
-    // ... and else until there are two CTAs of 256 threads per SM, while every thread keeps 8 elements
-    // (64 rows of 32000: 9 us against 13 us).
+    // ... and else until there are as many, while every thread keeps 8 elements
     int c = (a.V + 4095) / 4096;
     if (c <= MAX_CLUSTER) {
-        while (c < MAX_CLUSTER && a.B * c < 2 * sm_count() && a.V >= c * 2048) ++c;
+        while (c < MAX_CLUSTER && !enough(c) && a.V >= c * 2048) ++c;
         const int ept = (share(c) + 255) / 256;
         if (ept <= 4) return vec ? run<256, 4, true>(L, a, c, share(c)) : run<256, 4, false>(L, a, c, share(c));
         if (ept <= 8) return vec ? run<256, 8, true>(L, a, c, share(c)) : run<256, 8, false>(L, a, c, share(c));
         return vec ? run<256, 16, true>(L, a, c, share(c)) : run<256, 16, false>(L, a, c, share(c));
     }
-    // few rows of large vocabularies
-    const int ept = (share(MAX_CLUSTER) + 511) / 512;
+    // few rows of large vocabularies (4 rows of 131072: 8.5 us, by 512 threads with 64 elements 11.7 us)
     c = MAX_CLUSTER;
-    if (ept <= 16) return vec ? run<512, 16, true>(L, a, c, share(c)) : run<512, 16, false>(L, a, c, share(c));
+    if (share(c) <= 512 * 16) return vec ? run<512, 16, true>(L, a, c, share(c)) : run<512, 16, false>(L, a, c, share(c));
+    if (c1 <= c) return vec ? run<256, 64, true>(L, a, c, share(c)) : run<256, 64, false>(L, a, c, share(c));
     return vec ? run<512, 64, true>(L, a, c, share(c)) : run<512, 64, false>(L, a, c, share(c));
 }
 

@@ -194,7 +194,8 @@ def test_strides_and_alignment(offset):
     assert bool((whole == 77).all())
 
 
-@pytest.mark.parametrize("V,B", [(512, 2), (2000, 3), (8000, 300), (20000, 160), (30000, 2), (60000, 2), (200000, 1)])
+@pytest.mark.parametrize("V,B", [(512, 2), (2000, 3), (4000, 3), (8000, 300), (20000, 160), (30000, 2), (60000, 2), (100000, 2),
+                                 (200000, 1)])
 def test_unaligned_rows_of_every_size(V, B):
     """Rows at odd addresses, with all that a call can have, for every split of a row."""
     hist = 40
