@@ -626,20 +626,23 @@ __global__ void __launch_bounds__(MMA_WARPS * 32, F32Shape<HD>::CTAS) k_paged_f3
 // Where the items alone would leave half the GPU idle they are cut into one unit for each of the
 // `resident` CTAs (one sequence of 32000, 8 key heads of 128: 35 us, in nine pieces per SM 53 us), else
 // into about nine per SM, so that ragged ones end together (32 contexts up to 16000: 185 us, in three per
-// SM 216 us).  No unit is shorter than 256 keys; where there are items enough to go round (128 at a head
-// width of 128, 64 at 64), none is shorter than 1024, because joining costs a launch and the cut items'
-// states.  (Contexts up to 1000, 8 key heads of 128: one sequence takes 12.6 us with pieces of 256 and
-// 17.4 whole, 256 sequences take 139 us and 118.)
-UnitPlan make_plan(const PagedArgs& p, int H, int hd, int rt, int rows_lo, int rows_hi, int resident) {
+// SM 216 us).  No unit is shorter than 256 keys, and where the items go round none is shorter than 1024,
+// because joining costs a launch and the cut items' states.  (8 key heads of 128: 24 contexts up to 2000
+// take 30 us with pieces of 256 and 34 us of 1024, 256 contexts up to 1000 take 139 us and 118 us.)  In
+// float32 a key costs more and a row's join less beside it: few rows are cut until there is an item for
+// every CTA (240 contexts and heads of 64 up to 2000: 48 us, in pieces of 1024 59 us; with tiles full of
+// rows 50 us in place of 55 the other way round).
+UnitPlan make_plan(const PagedArgs& p, int H, int rt, int rows_lo, int rows_hi, int resident) {
     UnitPlan u;
     u.g = H / p.Hkv;
     u.rt = rt;
     u.rows_lo = rows_lo;
     u.rows_hi = rows_hi;
     const long long items = plan_items(p, u);
-    u.min_chunk = items >= hd ? 1024 : 256;
+    const bool idle = 2 * items < resident, few_rows = (long long)p.max_q * u.g <= F32Shape<16>::RT / 2;
+    u.min_chunk = idle || (rt == F32Shape<16>::RT && few_rows && items < resident) ? 256 : 1024;
     u.chunk_align = 64;
-    u.target = 2 * items < resident ? resident : 9 * sm_count();
+    u.target = idle ? resident : 9 * sm_count();
     u.slots = (int)plan_slots(p, u);
     u.part = 0;
     return u;
@@ -651,7 +654,7 @@ int resident_ctas(int hd) {
     return sm_count() * (hd == 16 ? Shape<16>::CTAS : hd == 32 ? Shape<32>::CTAS : hd == 64 ? Shape<64>::CTAS : Shape<128>::CTAS);
 }
 UnitPlan f32_plan(const PagedArgs& p, int H, int hd) {
-    return make_plan(p, H, hd, 8, 1, ANY, resident_ctas<F32Shape>(hd));
+    return make_plan(p, H, F32Shape<16>::RT, 1, ANY, resident_ctas<F32Shape>(hd));
 }
 
 // bf16: sequences of at most FEW_ROWS rows per key head go to the warp-level kernel, those of more
@@ -670,7 +673,7 @@ Bf16Plans bf16_plans(const PagedArgs& p, int H, int hd) {
            (((long long)p.n_pages * 2 * p.Hkv) << p.page_shift) < (1LL << 31);
     PagedArgs few = p;              // its bounds
     if (b.tc) few.max_q = FEW_ROWS / g < 1 ? 1 : FEW_ROWS / g;
-    b.u_mma = make_plan(few, H, hd, 16, 1, b.tc ? FEW_ROWS : ANY, resident_ctas<MmaShape>(hd));
+    b.u_mma = make_plan(few, H, 16, 1, b.tc ? FEW_ROWS : ANY, resident_ctas<MmaShape>(hd));
     b.floats = (size_t)b.u_mma.slots * b.u_mma.rt * (hd + 2);
     b.u_tc = {};
     if (b.tc) {

@@ -29,8 +29,8 @@
  *     is the legacy default stream).  Argument errors are detected on the host before
  *     anything is launched and returned synchronously; nothing is then modified.
  *   - Device-side checks (token id out of range, a state that does not match its
- *     registered position, a page outside its pool) latch a flag in the model's device header; the next
- *     rlt_last_error() call reports and clears it.
+ *     registered position, a page outside its pool) latch a flag in the model's device
+ *     header; the next rlt_last_error() call reports and clears it.
  *   - A model handle is not re-entrant: calls on one handle must be serialised by the
  *     caller.  Distinct handles are independent.
  *   - dtype RLT_F32 stores weights, e, M and the SWA cache in float32; RLT_BF16 stores
@@ -300,7 +300,7 @@ typedef struct {
     const int32_t* tokens;      /* device, or NULL: token i of row b's history is at
                                  * tokens[b * seq_stride + i * tok_stride]                       */
     int64_t seq_stride, tok_stride;
-    int32_t n_tokens;           /* largest history, >= 0                                         */
+    int32_t n_tokens;           /* largest history, >= 0; so many are readable in every row       */
     const int32_t* tok_len;     /* device [B]: the rows' histories, or NULL: n_tokens each       */
     const int32_t* gen_start;   /* device [B]: where the prompt ends, or NULL: 0                 */
     const float* repetition;    /* device [B] or NULL, each of the four; > 0                     */
