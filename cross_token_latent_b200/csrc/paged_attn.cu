@@ -61,9 +61,9 @@ __device__ __forceinline__ void join_row(T* o, int hd, int n, const float* __res
 
 // Joins the partial states of the cut items.  The first n1 blocks of x are cut items of the plan u,
 // whose rows the first y1 blocks of y take in turn.  With the plan us, block n1 + c - 1 is the item that
-// share c begins inside of, if share c is the first to: 128 rows, a thread each, of 8 columns (y: column
-// and row blocks).
-constexpr int JOIN_COLS = 8;
+// share c begins inside of, if share c is the first to: 128 rows, a thread each, of 16 columns (y: column
+// and row blocks; 9 turns with heads of 64 take 98 us in all with 8 columns, 95 with 16, 96 with 32).
+constexpr int JOIN_COLS = 16;
 template <typename T>
 __global__ void __launch_bounds__(JOIN_THREADS) k_paged_join(PagedArgs p, PagedAttnArgs a, UnitPlan u, int n1,
                                                              int y1, SharePlan us) {
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_paged_join(PagedArgs p, PagedA
     float m = NEG_BIG, l = 0.f, acc[JOIN_COLS];
 #pragma unroll
     for (int k = 0; k < JOIN_COLS; ++k) acc[k] = 0.f;
-    constexpr int AHEAD = 4;                    // states whose loads are in flight together
+    constexpr int AHEAD = 2;                    // states whose loads are in flight together
     for (int j0 = 0; j0 < n; j0 += AHEAD) {
         float v[AHEAD][JOIN_COLS], mj[AHEAD], lj[AHEAD];
         float to = m;
