@@ -18,11 +18,12 @@
 // maximum moves only when it grew by more than 2^8 (RESCALE): a smaller maximum is as good a
 // reference for the exponentials, and the accumulator then seldom has to be rescaled; a stage's O is
 // final when its next scores have arrived, because its MMAs complete in order.
-// Probabilities are rounded to bf16 for the product, as the tensor core takes them (2^-9 each, which
-// averages out over the keys); their sum is of the float32 values, and O, maximum and sum stay float32.
-// What bounds it is the softmax: 8192 tokens of 16 heads of 128 behind 8192 others take 716 us, 1150
-// TFLOP/s or 70 % of the tensor cores' measured rate (845 us once the board's power limit lowers the
-// clocks); heads of 64 take 522 us for half the operations, 606 us with one CTA per SM.
+// Probabilities are rounded to bf16 for the product, as the tensor core takes them (2^-8 each at most), and
+// their sum is of the rounded values, so that the result stays a weighted mean of the values (a row of few
+// keys was off by up to 2^-8 more with the sum of the unrounded ones, which took 716 us for the long chunk
+// below).  O, maximum and sum are float32.
+// What bounds it is the softmax: 8192 tokens of 16 heads of 128 behind 8192 others take 737 us, 1120
+// TFLOP/s or 68 % of the tensor cores' measured rate; heads of 64 take 560 us for half the operations.
 // Every mbarrier wait is bounded.
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -90,8 +91,17 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
     return r;
 }
 
+// s += the two bf16 halves of w, in float32.  (Shifting and masking them into place: 746 us in place of 737
+// for the long chunk, 570 in place of 560 with heads of 64.)
+__device__ __forceinline__ void add_bf16x2(float2& s, uint32_t w) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+        : "+f"(s.x), "+f"(s.y)
+        : "r"(w));
+}
+
 // Probabilities of 32 scores (of scaled scores less the maximum, bf16, two to a word) into the TMEM
-// columns at t_p, and their sum.  POLY of every 8 pairs take the polynomial.
+// columns at t_p, and the sum of what was stored.  POLY of every 8 pairs take the polynomial.
 template <int POLY>
 __device__ __forceinline__ float softmax32(const uint32_t (&x)[32], uint32_t t_p, float c2, float neg) {
     const float2 cc = make_float2(c2, c2), nn = make_float2(neg, neg);
@@ -108,7 +118,7 @@ __device__ __forceinline__ float softmax32(const uint32_t (&x)[32], uint32_t t_p
         }
         __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
         pk[i] = *reinterpret_cast<uint32_t*>(&h);
-        sum[i & 1] = add2(sum[i & 1], y);
+        add_bf16x2(sum[i & 1], pk[i]);
     }
     tmem_st16_async(t_p, pk);
     sum[0] = add2(sum[0], sum[1]);
