@@ -22,8 +22,8 @@
 // their sum is of the rounded values, so that the result stays a weighted mean of the values (a row of few
 // keys was off by up to 2^-8 more with the sum of the unrounded ones, which took 716 us for the long chunk
 // below).  O, maximum and sum are float32.
-// What bounds it is the softmax: 8192 tokens of 16 heads of 128 behind 8192 others take 737 us, 1120
-// TFLOP/s or 68 % of the tensor cores' measured rate; heads of 64 take 560 us for half the operations.
+// What bounds it is the softmax: 8192 tokens of 16 heads of 128 behind 8192 others take 738 us, 1117
+// TFLOP/s or 68 % of the tensor cores' measured rate; heads of 64 take 561 us for half the operations.
 // Every mbarrier wait is bounded.
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -124,15 +124,23 @@ __device__ __forceinline__ float softmax32(const uint32_t (&x)[32], uint32_t t_p
     sum[0] = add2(sum[0], sum[1]);
     return sum[0].x + sum[0].y;
 }
+// The greater of the two, or NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+// Greatest of 32 scores, NaN if one is.
 __device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
     float m[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        m[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
+        m[e] = max_nan(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
 #pragma unroll
-        for (int i = 8; i < 32; i += 8) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4])));
+        for (int i = 8; i < 32; i += 8)
+            m[e] = max_nan(m[e], max_nan(__uint_as_float(x[i + e]), __uint_as_float(x[i + e + 4])));
     }
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    return max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
 }
 // Columns behind `seen` of 32 scores become -inf.
 __device__ __forceinline__ void mask32(uint32_t (&x)[32], int seen) {
@@ -355,14 +363,16 @@ k_paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     for (int k = 0; k < KEEP; ++k) {
                         tmem_wait_ld(x[k]);
                         if (masked) mask32(x[k], seen - 32 * (c + k));
-                        mx = fmaxf(mx, max32(x[k]));
+                        mx = max_nan(mx, max32(x[k]));
                     }
                 }
                 mx *= c2;
                 // (a first maximum needs no rescale: the first product overwrites O, and l is 0)
-                const bool grow = mx > m + RESCALE || m == -INFINITY;
+                const bool grow = !(mx <= m + RESCALE) || m == -INFINITY;
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float to = grow ? mx : m;
+                    // A score that is NaN, or +inf (inf - inf is NaN), makes the row NaN from here on: the
+                    // polynomial's clamp would lose it.
+                    const float to = mx == INFINITY ? __int_as_float(0x7fffffff) : grow ? mx : m;
                     const float al = m == -INFINITY ? 1.f : ex2_approx(m - to);
                     l *= al;
                     m = to;

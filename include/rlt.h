@@ -204,7 +204,8 @@ rlt_status rlt_sample(rlt_model* m, const float* logp, int B, const float* u, in
  * starts, kv_len below the number of new tokens) or in a table entry outside [0, n_pages) latches
  * RLT_EDEVICE: such a sequence is left out; a key behind such an entry reads page 0 and an append
  * to one is dropped.  Values (and keys) in slots at and behind kv_len are never used, whatever
- * they hold; those of a sequence's own tokens must be finite, and scores within +-1e30. */
+ * they hold; values of a sequence's own tokens must be finite, and finite scores within +-1e30.  A row
+ * that has a NaN or +inf among its scores is NaN throughout; no other row is touched by it. */
 typedef struct {
     int32_t B;                  /* sequences, >= 1                                             */
     int32_t N;                  /* packed rows, >= 1                                           */
