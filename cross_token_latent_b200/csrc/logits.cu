@@ -20,6 +20,8 @@
 // The history is counted into shared memory with integer atomics, whose order cannot change a count.
 // Of a token's occurrences the one that comes first then changes its logit, so that the steps over the
 // whole row know nothing of penalties (looking at every element's counter took 47 us in place of 44).
+#include <cfloat>
+
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -87,6 +89,9 @@ __device__ __forceinline__ LogitsRow load_row(const LogitsArgs& a, int b) {
             a.gen_start ? a.gen_start[b] : 0};
 }
 
+// A repetition or a temperature: a normal number above 0, so that its reciprocal is finite.
+__device__ __forceinline__ bool factor_ok(float x) { return x >= FLT_MIN && x <= FLT_MAX; }
+
 template <int LT, int EPT, bool VEC>
 __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process_logits(LogitsArgs a, int slice, int n_cta) {
     using S = LogitsShape<LT, EPT, VEC>;
@@ -135,14 +140,17 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
 
     for (int round = 0; b < a.B; b += clusters, ++round) {
         bool bad = false;
-        if (!(row.rep > 0.f)) { row.rep = 1.f; bad = true; }
-        if (!(row.tau > 0.f)) { row.tau = 1.f; bad = true; }
+        if (!factor_ok(row.rep)) { row.rep = 1.f; bad = true; }
+        if (!factor_ok(row.tau)) { row.tau = 1.f; bad = true; }
         if (row.len < 0 || row.len > a.n_tokens) { row.len = min(max(row.len, 0), a.n_tokens); bad = a.tokens || bad; }
         const float inv_tau = 1.0f / row.tau, inv_rep = 1.0f / row.rep, lse_in = row.lse;
+        const float to_log2 = inv_tau * LOG2E;                  // (inv_tau is 2^126 at most)
         // Less the input's log-sum-exp, as x is: only penalties need it, the softmax does not.
         auto penalise = [&](float x, uint32_t c) {
             x += lse_in;
-            x *= x > 0.f ? inv_rep : row.rep;
+            const float y = x * (x > 0.f ? inv_rep : row.rep);
+            // what the penalty takes out of float32's range stays at its end
+            x = isinf(y) && !isinf(x) ? copysignf(FLT_MAX, x) : y;
             if (c > 0) x -= row.presence + row.frequency * (float)c;
             return x - lse_in;
         };
@@ -222,12 +230,6 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
                 for (int j = 0; j < W; ++j) x[i + j] += bi[j];
             }
         }
-#pragma unroll
-        for (int i = 0; i < EPT; i += 2) {
-            const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(inv_tau, inv_tau));
-            x[i] = y.x;
-            x[i + 1] = y.y;
-        }
         if (a.mask) {
 #pragma unroll
             for (int i = 0; i < EPT; i += W) {
@@ -260,8 +262,8 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < EPT; i += 2) {
-            // (safe * LOG2E may overflow)
-            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-safe, -safe)), make_float2(LOG2E, LOG2E));
+            // the maximum is taken off before the scale: neither x / tau nor safe / tau need be in range
+            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-safe, -safe)), make_float2(to_log2, to_log2));
             sum = add2(sum, make_float2(ex2_approx(y.x), ex2_approx(y.y)));
         }
         float s = warp_sum(sum.x + sum.y);
@@ -283,13 +285,13 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
         m = warp_max(m);
         const float top = m == -INFINITY ? 0.f : m;
         s = 0.f;
-        for (int i = lane; i < n_cta * LW; i += 32) s += all[i].y * ex2_approx((all[i].x - top) * LOG2E);
+        for (int i = lane; i < n_cta * LW; i += 32) s += all[i].y * ex2_approx((all[i].x - top) * to_log2);
         s = warp_sum(s);
         // No token allowed: all -inf.  (A NaN leaves no sum of zero, and the row is NaN.)
         const bool empty = m == -INFINITY && s == 0.f;
         const float log_s = (empty ? 0.f : logf(s)) + (lse_in - lse_in);        // (NaN where lse is)
         if (rank == 0 && tid == 0) {
-            if (a.out_lse) a.out_lse[b] = m + log_s + lse_in * inv_tau;
+            if (a.out_lse) a.out_lse[b] = (m + lse_in) * inv_tau + log_s;
             if (empty) raise_flag(a.hdr, ERR_BAD_LOGITS);
         }
         if (empty) m = 0.f;                                     // (its elements are -inf as they are)
@@ -298,14 +300,14 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
         for (int i = 0; i < EPT; i += W) {
             const int e = i * LT + tid * W;
             if (e >= n) continue;
-            // (m + log_s may round log_s away)
+            // (m / tau + log_s may round log_s away)
             if (VEC) {
-                const float2 mm = make_float2(-m, -m), ll = make_float2(-log_s, -log_s);
-                const float2 y0 = add2(add2(make_float2(x[i], x[i + 1]), mm), ll);
-                const float2 y1 = add2(add2(make_float2(x[i + W / 2], x[i + W - 1]), mm), ll);
+                const float2 mm = make_float2(-m, -m), tt = make_float2(inv_tau, inv_tau), ll = make_float2(-log_s, -log_s);
+                const float2 y0 = fma2(add2(make_float2(x[i], x[i + 1]), mm), tt, ll);
+                const float2 y1 = fma2(add2(make_float2(x[i + W / 2], x[i + W - 1]), mm), tt, ll);
                 __stcs(reinterpret_cast<float4*>(o + e), make_float4(y0.x, y0.y, y1.x, y1.y));
             } else {
-                o[e] = x[i] - m - log_s;
+                o[e] = fmaf(x[i] - m, inv_tau, -log_s);
             }
         }
     }

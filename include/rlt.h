@@ -304,17 +304,19 @@ typedef struct {
     int32_t n_tokens;           /* largest history, >= 0; so many are readable in every row       */
     const int32_t* tok_len;     /* device [B]: the rows' histories, or NULL: n_tokens each       */
     const int32_t* gen_start;   /* device [B]: where the prompt ends, or NULL: 0                 */
-    const float* repetition;    /* device [B] or NULL, each of the four; > 0                     */
+    const float* repetition;    /* device [B] or NULL, each of the four; > 0, normal             */
     const float* presence;
     const float* frequency;
-    const float* tau;           /* > 0                                                           */
+    const float* tau;           /* > 0, normal                                                   */
     float* out_lse;             /* device [B] or NULL: log sum exp z                             */
 } rlt_logits;
 
 /* One launch; vectors of 16 bytes where x, out and bias are 16-byte aligned with strides that are
  * multiples of 4.  A row that the mask leaves without a token becomes -inf throughout and latches
  * RLT_EDEVICE, as do history ids outside [0, V) (skipped), lengths outside [0, n_tokens] (clamped)
- * and a repetition or tau that is not above 0 (taken as 1).
+ * and a repetition or tau that is no normal number above 0 (taken as 1).  A logit that the repetition
+ * takes out of float32's range stays at the range's end; the softmax takes the row's maximum off before
+ * it divides by tau, so that any tau is safe.
  * Errors: RLT_EINVAL, RLT_EUNSUPPORTED (V above 262144), RLT_ECUDA. */
 rlt_status rlt_process_logits(rlt_model* m, const rlt_logits* a, int B, void* stream);
 
