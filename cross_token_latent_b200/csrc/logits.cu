@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(LT, LogitsShape<LT, EPT, VEC>::CTAS) k_process
         bool bad = false;
         if (!factor_ok(row.rep)) { row.rep = 1.f; bad = true; }
         if (!factor_ok(row.tau)) { row.tau = 1.f; bad = true; }
-        if (row.len < 0 || row.len > a.n_tokens) { row.len = min(max(row.len, 0), a.n_tokens); bad = a.tokens || bad; }
+        if (row.len < 0 || row.len > a.n_tokens) { row.len = min(max(row.len, 0), a.n_tokens); bad = true; }
         const float inv_tau = 1.0f / row.tau, inv_rep = 1.0f / row.rep, lse_in = row.lse;
         const float to_log2 = inv_tau * LOG2E;                  // (inv_tau is 2^126 at most)
         // Less the input's log-sum-exp, as x is: only penalties need it, the softmax does not.

@@ -1373,7 +1373,7 @@ rlt_status rlt_process_logits(rlt_model* m, const rlt_logits* a, int B, void* st
     g.x = a->x; g.x_stride = a->x_stride; g.out = a->out; g.out_stride = a->out_stride; g.B = B; g.V = V;
     g.lse = a->lse; g.bias = a->bias; g.bias_stride = a->bias_stride; g.mask = a->mask; g.mask_stride = a->mask_stride;
     g.tokens = a->n_tokens > 0 ? a->tokens : nullptr;
-    g.seq_stride = a->seq_stride; g.tok_stride = a->tok_stride; g.n_tokens = a->n_tokens;
+    g.seq_stride = a->seq_stride; g.tok_stride = a->tok_stride; g.n_tokens = a->tokens ? a->n_tokens : 0;
     g.tok_len = a->tok_len; g.gen_start = a->gen_start; g.repetition = a->repetition; g.presence = a->presence;
     g.frequency = a->frequency; g.tau = a->tau; g.out_lse = a->out_lse; g.hdr = m->hdr();
     Launch L = m->launch(stream);

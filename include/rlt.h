@@ -313,10 +313,10 @@ typedef struct {
 
 /* One launch; vectors of 16 bytes where x, out and bias are 16-byte aligned with strides that are
  * multiples of 4.  A row that the mask leaves without a token becomes -inf throughout and latches
- * RLT_EDEVICE, as do history ids outside [0, V) (skipped), lengths outside [0, n_tokens] (clamped)
- * and a repetition or tau that is no normal number above 0 (taken as 1).  A logit that the repetition
- * takes out of float32's range stays at the range's end; the softmax takes the row's maximum off before
- * it divides by tau, so that any tau is safe.
+ * RLT_EDEVICE, as do history ids outside [0, V) (skipped), lengths outside [0, n_tokens], without
+ * tokens outside [0, 0] (clamped), and a repetition or tau that is no normal number above 0 (taken as
+ * 1).  A logit that the repetition takes out of float32's range stays at the range's end; the softmax
+ * takes the row's maximum off before it divides by tau, so that any tau is safe.
  * Errors: RLT_EINVAL, RLT_EUNSUPPORTED (V above 262144), RLT_ECUDA. */
 rlt_status rlt_process_logits(rlt_model* m, const rlt_logits* a, int B, void* stream);
 
