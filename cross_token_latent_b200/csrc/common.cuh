@@ -16,7 +16,7 @@ enum : uint32_t {
     ERR_STATE_MISMATCH = 2u,// a state header disagreed with its registered position/version
     ERR_TIMEOUT = 4u,       // a bounded device wait gave up
     ERR_BAD_PAGE = 8u,      // a page id, or a sequence's lengths, outside what the call was told
-    ERR_BAD_LOGITS = 16u,   // a mask that leaves a row without a token, or a parameter out of range
+    ERR_BAD_LOGITS = 16u,   // a row without a token (masked, or to be drawn from), or a parameter out of range
 };
 
 struct DevHeader {          // first 256 bytes of the weight arena

@@ -256,7 +256,7 @@ int sample_max_vocab();
 // tokens in id order.  tok[b * tok_stride] = the draw, blp[b] (optional) = its log-probability
 // under the truncated, renormalised distribution.
 cudaError_t launch_sample(Launch L, const float* logp, int B, int V, const float* u, int top_k, float top_p,
-                          int32_t* tok, int tok_stride, float* blp);
+                          int32_t* tok, int tok_stride, float* blp, DevHeader* hdr);
 
 // ------------------------------------------------------------------ small_step.cu
 // The whole decoder step of a small model in one launch, one CTA per sequence.

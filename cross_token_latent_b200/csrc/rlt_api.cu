@@ -1266,7 +1266,7 @@ rlt_status rlt_sample(rlt_model* m, const float* logp, int B, const float* u, in
         return RLT_EINVAL;
     if (m->cfg.V > sample_max_vocab()) return RLT_EUNSUPPORTED;
     Launch L = m->launch(stream);
-    CK(launch_sample(L, logp, B, m->cfg.V, u, top_k, top_p, tokens, tok_stride, behaviour_logp));
+    CK(launch_sample(L, logp, B, m->cfg.V, u, top_k, top_p, tokens, tok_stride, behaviour_logp, m->hdr()));
     return RLT_OK;
 }
 

@@ -10,7 +10,8 @@
 //   top-k   the k-th largest pattern, found by a 4-pass radix select (8-bit digits);
 //   top-p   the smallest pattern b with mass(pattern > b) < top_p * Z1, found by bisection.
 // The kept tokens are then scanned in id order (float64 sums) and the first id whose
-// cumulative kept mass exceeds u * Z is the draw.
+// cumulative kept mass exceeds u * Z is the draw.  A token without mass (-inf where a mask forbids it) is
+// never kept; a row without any mass gives token 0, a log-probability of -inf, and raises the flag.
 #include "kernels.cuh"
 
 namespace rlt {
@@ -38,7 +39,8 @@ __device__ __forceinline__ double block_sum_d(double v, double* red) {
 }
 
 __global__ void __launch_bounds__(ST) k_sample(const float* __restrict__ logp, int V, const float* __restrict__ u,
-                                               int top_k, float top_p, int32_t* tok, int tok_stride, float* blp) {
+                                               int top_k, float top_p, int32_t* tok, int tok_stride, float* blp,
+                                               DevHeader* hdr) {
     extern __shared__ uint32_t bits[];       // V patterns of p = exp(logp)
     __shared__ int hist[256];
     __shared__ double red[SW];
@@ -100,6 +102,8 @@ __global__ void __launch_bounds__(ST) k_sample(const float* __restrict__ logp, i
         if (lo > thr) thr = lo;
     }
 
+    if (thr == 0) thr = 1;                   // (the pattern of the smallest mass above zero)
+
     // inverse CDF over the kept tokens in id order: thread k scans ids [c0, c1)
     const int per = (V + ST - 1) / ST;
     const int c0 = min(V, (int)threadIdx.x * per), c1 = min(V, c0 + per);
@@ -145,9 +149,11 @@ __global__ void __launch_bounds__(ST) k_sample(const float* __restrict__ logp, i
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        const int x = found >= 0 ? found : 0;        // a kept set is never empty; guards a NaN u
+        const bool any = total > 0.0;                // no: all -inf, or a NaN
+        const int x = any && found >= 0 ? found : 0;
         tok[(long long)b * tok_stride] = x;
-        if (blp) blp[b] = (float)((double)row[x] - log(total));
+        if (blp) blp[b] = total == 0.0 ? -INFINITY : (float)((double)row[x] - log(total));
+        if (!any) raise_flag(hdr, ERR_BAD_LOGITS);
     }
 }
 
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(ST) k_sample(const float* __restrict__ logp, i
 int sample_max_vocab() { return 49152; }
 
 cudaError_t launch_sample(Launch L, const float* logp, int B, int V, const float* u, int top_k, float top_p,
-                          int32_t* tok, int tok_stride, float* blp) {
+                          int32_t* tok, int tok_stride, float* blp, DevHeader* hdr) {
     const size_t smem = (size_t)V * 4;
     static bool attr_set = false;
     if (!attr_set) {
@@ -165,7 +171,7 @@ cudaError_t launch_sample(Launch L, const float* logp, int B, int V, const float
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    return launch_k(L, k_sample, (unsigned)B, ST, smem, logp, V, u, top_k, top_p, tok, tok_stride, blp);
+    return launch_k(L, k_sample, (unsigned)B, ST, smem, logp, V, u, top_k, top_p, tok, tok_stride, blp, hdr);
 }
 
 }  // namespace rlt

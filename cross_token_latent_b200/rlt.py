@@ -429,7 +429,8 @@ class RLTModel:
     def sample(self, logp: torch.Tensor, u: torch.Tensor, top_k: int = 0, top_p: float = 1.0,
                out: torch.Tensor | None = None, behaviour_logp: torch.Tensor | None = None) -> torch.Tensor:
         """rlt_sample: one token per row of logp [B, V] with the uniforms u [B]; `out` may be a
-        column view of a token matrix (its stride is passed through)."""
+        column view of a token matrix (its stride is passed through).  A row without any probability
+        gives token 0 with a log-probability of -inf and latches RLT_EDEVICE."""
         B = logp.shape[0]
         out = torch.empty(B, dtype=torch.int32, device=self.device) if out is None else out
         _check(lib().rlt_sample(self.handle, _ptr(logp), B, _ptr(u), int(top_k), float(top_p), _ptr(out),
@@ -598,12 +599,14 @@ class RLTModel:
         incrementally, step].  uniforms: float device [n_new, B].  Returns (tokens [B, P + n_new]
         int32, behaviour log-probs [B, n_new], prompt log-probs [B, P - 1] (entry t-1 = log p of
         x_{t+1}), the state after all P + n_new tokens).  Every step of the loop runs in the
-        library's kernels; nothing is copied to the host.
+        library's kernels; nothing but the error flag of a controlled call is copied to the host.
 
         With any of repetition, presence, frequency (numbers, or float32 device vectors [B]), bias
         (float32 [B or 1, V]) and mask (int32 [B or 1, ceil(V / 32)], or a function of the number of
         tokens generated so far and the tokens [B, t] that returns one) each draw is from the logits
-        that process_logits makes of them: the prompt counts for repetition only."""
+        that process_logits makes of them: the prompt counts for repetition only.  What the device
+        refused on the way, a row without an allowed token among it, is raised as RLTError at the end
+        (of a captured call last_error() tells behind the replay)."""
         prompt = prompt.to(device=self.device, dtype=torch.int32).contiguous()
         B, P = prompt.shape
         T = P + n_new
@@ -636,6 +639,8 @@ class RLTModel:
             self.sample(row, uniforms[t - P], top_k, top_p, out=toks[t], behaviour_logp=blp[t - P])
             self.encode_append(toks[t], t, cache, T, e, M)
         self.decode_step(st, e, M, tau=tau)         # the transition of x_T
+        if control is not None and not torch.cuda.is_current_stream_capturing():
+            self.check_device_errors()
         return toks.t().contiguous(), blp.t().contiguous(), lp_prompt.t().contiguous(), st
 
     # ---------------------------------------------------------------- decoder

@@ -181,6 +181,9 @@ rlt_status rlt_encode_append(rlt_model* m, const int32_t* tokens, int tok_stride
  *                   exceeds u[b] times the kept total
  *   behaviour_logp  device float [B] or NULL: log of the draw's probability after truncation
  *                   and renormalisation
+ * Tokens without probability are never drawn.  A row of nothing else (all -inf: a mask that leaves no
+ * token) gives token 0 with a behaviour_logp of -inf, a row with a NaN token 0 with NaN; both latch
+ * RLT_EDEVICE.
  * Errors: RLT_EINVAL, RLT_EUNSUPPORTED (V above 49152: the row is staged in shared memory),
  * RLT_ECUDA. */
 rlt_status rlt_sample(rlt_model* m, const float* logp, int B, const float* u, int top_k, float top_p,
