@@ -17,6 +17,10 @@
 // 512 rows of 32768 with everything take 42 us by pairs of 256 threads with 64 elements each, 44 by 1024
 // with 16, one CTA per SM, and 76 without the copies ahead.
 //
+// Divisions by the temperature and the repetition are products with their reciprocals, and the sum's
+// exponentials are ex2.approx (2^-22 each): beside the formula's own float32 roundings both are small (error
+// against 64 bits 5e-8 of the norm in place of 4.4e-8 for one row of 512, 3.7e-8 and 3.9e-8 for 512 of 32768).
+//
 // The history is counted into shared memory with integer atomics, whose order cannot change a count.
 // Of a token's occurrences the one that comes first then changes its logit, so that the steps over the
 // whole row know nothing of penalties (looking at every element's counter took 47 us in place of 44).

@@ -200,7 +200,8 @@ __device__ __forceinline__ int share_keys(const SharePlan& u, const Seq& s, int 
 __device__ __forceinline__ int share_steps(const SharePlan& u, const Seq& s, int tile) {
     return u.whole ? 1 : (share_keys(u, s, tile) + STEP_KEYS - 1) / STEP_KEYS;
 }
-// Sum over i < n of floor((a i + b) / m), by Euclid's steps.
+// Sum over i < n of floor((a i + b) / m), reduced by the steps of Euclid's algorithm (sums of floors of an
+// arithmetic progression: Graham, Knuth, Patashnik, Concrete Mathematics, 3.5).
 __device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
     long long sum = 0;
     while (n > 0) {

@@ -198,6 +198,9 @@ struct MmaShape {
     static constexpr int SMEM = RING > JOIN ? RING : JOIN;
 };
 
+// (Narrow heads are bound by the instructions per key: 100 contexts of 500 to 8000 keys, 16 heads of 16, take
+// 132 us, half the copy rate, at 64 % issue.  Chunks read all keys again for every 16 rows, from L2: a prompt of
+// 2000 tokens takes 60 us with 16 heads of 32 and 44 us with heads of 16, 52 % issue.)
 template <int HD>
 __global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mma(PagedArgs p, PagedAttnArgs a, UnitPlan u,
                                                                                   int units) {
@@ -441,12 +444,15 @@ __global__ void __launch_bounds__(MMA_WARPS * 32, MmaShape<HD>::CTAS) k_paged_mm
 
 // ------------------------------------------------------------------ float32
 // 8 rows of one key head against groups of 16 keys, every warp on its own as above, on the CUDA cores
-// in float32 throughout (the tensor cores' formats would not hold the float32 model's results).  Lane
+// in float32 throughout (the tensor cores would need every operand split into several terms of their
+// formats, and a product for each pair of them: not tried).  Lane
 // 16 j + k scores key k for rows 4 j .. 4 j + 3 and then has columns k, k + 16, .. of the output of
 // those rows, the probabilities going round by shared memory.  Scoring, the four elements of a key that a
 // lane takes next are the (step + key)-th: side by side, keys lie HD floats apart, and lanes that all
-// took the same would meet in the same banks.  What bounds it is the products themselves, and in a
-// decode step the reading of the keys and values.
+// took the same would meet in the same banks.  What bounds it is a warp's chain per
+// 16 keys (wait, scores, maximum, exponentials, products): 6 chunks with heads of 16 take 22.6 us at 16 % of the
+// multiply-add pipe and 36 % issue; a decode step of 240 contexts with 8 heads of 64 takes 288 us, half the
+// measured copy rate, at 51 % issue, seven of eight rows of a tile being empty.
 template <int HD>
 struct F32Shape {
     static constexpr int RT = 8;

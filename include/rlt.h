@@ -247,8 +247,13 @@ size_t rlt_paged_attention_workspace_bytes(const rlt_model* m, const rlt_paged_b
 /* Causal attention of the batch's new tokens over the pool, which holds them already: row r at
  * position t reads keys 0..t of its sequence,
  *   out[r, h] = sum_j softmax_j(scale q[r, h] . K[j, h / g]) V[j, h / g],  g = n_heads / n_kv_heads,
- * with float32 softmax statistics and sums, rounded once to the model's dtype.  (On the tensor
- * cores the probabilities are rounded to bf16 as the encoder's own attention rounds them.)
+ * with float32 softmax statistics and sums, rounded once to the model's dtype.  In bf16 the tensor
+ * cores take the probabilities rounded to bf16 (2^-8 each at most), and the sum is of the rounded ones,
+ * so that out is a weighted mean of the values, as in the encoder's own attention.  Exponentials are
+ * exact to 2^-22, but with heads of 64 and 128 and more than 16 rows per key head a quarter of those
+ * away from the causal edge is taken by a polynomial of 2^-13.7 in front of that rounding.  The rows and
+ * keys that are taken together depend on the whole batch: the same batch gives the same bits, the same
+ * row in another batch the same numbers within these roundings.
  *   q, out      device rows [N, n_heads, head_dim] of the model's dtype (queries after the rotary
  *               embedding), q_stride / out_stride elements apart; 16-byte aligned, strides
  *               multiples of 8 and at least a row long
@@ -269,7 +274,9 @@ size_t rlt_encode_chunk_workspace_bytes(const rlt_model* m, const rlt_paged_batc
  * single generated token alike, ragged over the batch.  Every layer appends its keys and values
  * and attends over the cache; the new encoder outputs go to e[b, t] and their memory projections
  * to M[..., b, .., t, :] (layouts of rlt_encode, row capacity T_alloc), from where decoder steps
- * read them.  Equals the token-parallel encoding of the whole sequences up to summation order.
+ * read them.  In float32 it equals the token-parallel encoding of the whole sequences up to summation
+ * order; in bf16 up to the attention's rounding of probabilities too (rlt_paged_attention), so that a
+ * token's bits depend on how its sequence was cut into chunks and on what else was in the batch.
  *   tokens      device int32 [N]
  *   pools       L_E pools one after another, each rlt_page_pool_bytes(m, n_pages, page_size, n_heads) bytes
  * p->n_kv_heads must be the model's n_heads.  Requires max_kv <= T_alloc <= max_pos.  Out-of-range ids latch
